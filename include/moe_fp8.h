@@ -60,6 +60,7 @@ extern "C" {
 #define MOE_BF16 0
 #define MOE_F32 1
 #define MOE_E4M3FN 2
+#define MOE_MX4 3               /* microscaled 4-bit: see moe_quantize_rows_mx4 */
 
 /* activation-scale granularity */
 #define MOE_SCALE_ROW_DYNAMIC 0     /* one scale per row, from the row's absmax: [R] */
@@ -71,6 +72,10 @@ extern "C" {
 #define MOE_ACT_NONE 0
 #define MOE_ACT_SILU_MUL 1          /* quantize silu(x) * x_up (gated FFN) */
 
+/* router scores */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+
 /* operation ids for moe_workspace_bytes */
 #define MOE_OP_QUANTIZE_ROWS 0
 #define MOE_OP_SORT_BY_EXPERT 1
@@ -78,6 +83,8 @@ extern "C" {
 #define MOE_OP_TGMM 3
 #define MOE_OP_GATHER_REDUCE 4
 #define MOE_OP_QUANTIZE_WEIGHTS 5
+#define MOE_OP_GMM_MX4 6
+#define MOE_OP_FFN_TOKENS 7
 
 /* bits of the sticky device-error word (first int32 of a workspace) */
 #define MOE_DEVERR_EXPERT_ID 1      /* an expert id outside [0, E) */
@@ -531,11 +538,171 @@ int moe_silu_mul_backward(const void* a, const void* b, int64_t lda, const void*
                           void* da, void* db, int64_t ldo, void* stream);
 
 /*
+ * moe_router_topk -- the router in front of the sort: the k experts of every
+ * token and their weights, from the token's logits z [E].
+ *   scores   MOE_SCORE_SOFTMAX p_e = exp(z_e - m) / sum_f exp(z_f - m), or
+ *            MOE_SCORE_SIGMOID p_e = 1 / (1 + exp(-z_e))
+ *   choice   the k largest logits (scores rise with them), or with
+ *            select_bias the k largest p_e + select_bias[e], formed in 64
+ *            bits; in descending order, equal ones to the lower expert
+ *   weights  weight_scale * p_e of the chosen; with renormalize
+ *            weight_scale * p_e / (sum of the chosen p).  The bias enters the
+ *            choice only.
+ *
+ *   logits   [T, E] bf16 or f32 (logits_dtype), rows ldl >= E elements apart.
+ *            A logit of -inf (or NaN) takes the expert out for that token: it
+ *            is chosen after every other one and has weight 0.  A row without
+ *            any other logit (a padded token) gets experts 0 .. k-1 with
+ *            weights 0, so that every id stays valid for the sort.  A logit
+ *            of +inf is not supported (ids stay valid, weights unspecified).
+ *   select_bias optional [E] f32, finite (NULL for none).
+ *   expert_ids [T, k] int32 out; topk_weights [T, k] f32 out: what
+ *            moe_sort_by_expert, moe_gather_reduce and moe_ffn_tokens take.
+ * 1 <= E <= 1024, 1 <= k <= min(E, 64), weight_scale finite and > 0, T <=
+ * 2^31.  Needs no workspace.  Errors: MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED
+ * (type, score, renormalize not 0 or 1), MOE_ERR_NULL.
+ */
+int moe_router_topk(const void* logits, int logits_dtype, int64_t ldl, int64_t T, int32_t E, int32_t k, int score,
+                    const float* select_bias, int renormalize, float weight_scale, int32_t* expert_ids,
+                    float* topk_weights, void* stream);
+
+/*
+ * moe_router_topk_backward -- gradient of moe_router_topk's weights to the
+ * logits, the choice held fixed.  dweights is what moe_gather_reduce_backward
+ * writes as dw.  With g_j = weight_scale * dweights[t, j]:
+ *   softmax                dz_e = p_e (g_e - sum_j g_j p_j), g_e = 0 unless chosen
+ *   softmax, renormalize   dz_e = r_e (g_e - sum_j g_j r_j) for the chosen, 0
+ *                          for the others; r = the softmax over the chosen
+ *   sigmoid                dz_e = g_e p_e (1 - p_e)
+ *   sigmoid, renormalize   the same with (g_e - sum_j g_j p_j / S) / S in
+ *                          place of g_e, S = the chosen p's sum
+ * Experts taken out by -inf, and every expert of a row without another
+ * logit, get 0.
+ *   logits .. weight_scale as in the forward call; expert_ids [T, k] as it
+ *   wrote them (an id outside [0, E) takes no part; one given twice counts
+ *   twice).
+ *   dlogits  [T, E] out, logits_dtype, rows ldd >= E elements apart; must not
+ *            overlap logits.
+ * Sizes and errors as in moe_router_topk.
+ */
+int moe_router_topk_backward(const void* logits, int logits_dtype, int64_t ldl, const int32_t* expert_ids,
+                             const float* dweights, int64_t T, int32_t E, int32_t k, int score, int renormalize,
+                             float weight_scale, void* dlogits, int64_t ldd, void* stream);
+
+/*
+ * moe_quantize_rows_mx4 -- rows to the microscaled 4-bit format (the MXFP4
+ * of the OCP Microscaling Formats specification): every 32 consecutive
+ * elements share one e8m0 scale 2^(s - 127) and hold e2m1 codes (sign, two
+ * exponent bits, one mantissa bit; magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6).
+ *   scale    s = floor(log2(block absmax)) - 2 + 127, at least 0; 127 for a
+ *            block of zeros; 255 (NaN) for a block with an element that is
+ *            not finite: every element of it then reads back as NaN
+ *   codes    v / scale (exact) to the nearest e2m1 value, ties to the even
+ *            code, saturating at 6; the sign of zero is kept
+ *   x, x_up, ldx, act  [R, C] bf16, rows ldx elements apart, as in
+ *            moe_quantize_rows_strided (with MOE_ACT_SILU_MUL the matrix is
+ *            silu(x) * x_up in float32 by the same recipe).
+ *   q        [R, C/2] bytes out, rows ldq bytes apart: element 2i in the low
+ *            half of byte i, 2i + 1 in the high half.
+ *   scale    [R, C/32] bytes out, rows lds bytes apart.  q and scale may be
+ *            parts of one row (scale = q + C/2, ldq = lds), which one gather
+ *            then moves; bytes between the rows' parts are not written.
+ * C a multiple of 32, ldx >= C and a multiple of 8, ldq >= C/2 and a multiple
+ * of 16, lds >= C/32; x, x_up, q 16-byte aligned (MOE_ERR_SHAPE otherwise).
+ * Expert weights stored [E, N, K] are rows too (R = E N, C = K).  Needs no
+ * workspace.  Errors as in moe_quantize_rows_strided.
+ */
+int moe_quantize_rows_mx4(const void* x, const void* x_up, int64_t ldx, int act, int64_t R, int64_t C, uint8_t* q,
+                          int64_t ldq, uint8_t* scale, int64_t lds, void* stream);
+
+/*
+ * moe_quantize_weights_mx4 -- expert weights w [E, K, N] bf16 to the 4-bit
+ * format with blocks along the contraction K, stored contraction-contiguous:
+ * q [E, N, K/2], scale [E, N, K/32] (the layout moe_gmm_mx4 and
+ * moe_ffn_tokens read).  K a multiple of 32, N of 16; w and q 16-byte
+ * aligned.  Setup-time call; needs no workspace.  Errors: MOE_ERR_SHAPE,
+ * MOE_ERR_NULL; E = 0 returns MOE_OK.
+ */
+int moe_quantize_weights_mx4(const void* w, int64_t E, int64_t K, int64_t N, uint8_t* q, uint8_t* scale, void* stream);
+
+/*
+ * moe_dequantize_rows_mx4 -- the values of 4-bit rows, exactly.
+ *   q, ldq, scale, lds as moe_quantize_rows_mx4 writes them; out [R, C] bf16
+ *   (also for MOE_DTYPE_DEFAULT) or f32, rows ldo elements apart (ldo >= C, a
+ *   multiple of 8), 16-byte aligned.  A block of scale code 255 reads as NaN.
+ * Errors: MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_NULL.
+ */
+int moe_dequantize_rows_mx4(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t lds, int64_t R, int64_t C,
+                            int out_dtype, void* out, int64_t ldo, void* stream);
+
+/*
+ * moe_gmm_mx4 -- moe_gmm_fp8 with 4-bit weights: for local group g (rows as
+ * there)
+ *   out[r, c] = ls[r] * sum_k X[r, k] * W_g[k, c]
+ * accumulated in float32 by the scaled matrix cores, rounded once to
+ * out_dtype; rows past the last local group's are zero.
+ *   lhs      lhs_format MOE_E4M3FN: [M, K] e4m3fn, rows ldl bytes apart, with
+ *            lhs_scale f32 [M] (MOE_SCALE_ROW_DYNAMIC) or [1] (the tensor
+ *            modes) and lds = 0.
+ *            lhs_format MOE_MX4: [M, K/2] codes, rows ldl bytes apart, and
+ *            lhs_scale [M, K/32] e8m0 bytes, rows lds apart
+ *            (moe_quantize_rows_mx4; lhs_scale_mode MOE_SCALE_ROW_DYNAMIC).
+ *            Sorted rows of either kind come from moe_sort_by_expert /
+ *            moe_sort_gather_rows, which move bytes.
+ *   rhs      [E_loc, N, K/2] codes, rhs_scale [E_loc, N, K/32] e8m0 bytes
+ *            (moe_quantize_weights_mx4).
+ *   group_sizes .. num_local_experts, out, out_dtype as in moe_gmm_fp8.
+ *   ws       workspace of moe_workspace_bytes(MOE_OP_GMM_MX4, M, K, N, E).
+ * K a multiple of 32, N of 16, ldl a multiple of 16 and at least a row's
+ * bytes; lhs, rhs, out 16-byte aligned.  Errors as in moe_gmm_fp8.
+ */
+int moe_gmm_mx4(const uint8_t* lhs, int64_t ldl, const void* lhs_scale, int64_t lds, int lhs_format,
+                int lhs_scale_mode, const uint8_t* rhs, const uint8_t* rhs_scale, const int32_t* group_sizes, int32_t E,
+                int32_t group_offset, int32_t num_local_experts, int64_t M, int64_t K, int64_t N, int out_dtype,
+                void* out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_ffn_tokens -- a whole gated expert layer for a few tokens (decoding):
+ *   out[t, :] = sum_j w[t, j] * ((silu(x[t] W0_e) * (x[t] W1_e)) Wo_e), e = expert_ids[t, j]
+ * over the slots whose expert is local, in slot order; a token without one
+ * gets zeros.  The sorted path (quantize, sort, grouped matmuls, combine) is
+ * for many tokens; here the rows are not sorted and nothing is quantized: the
+ * activations stay bfloat16, sums and the hidden values 32-bit (the hidden
+ * values enter the second product as two bfloat16 pieces), one rounding at
+ * the end.  A token's result does not depend on the other tokens' values.
+ *   x        [T, H] bf16, rows ldx elements apart (a multiple of 8, 16-byte
+ *            aligned); 0 <= T <= 64, T k <= 1024 (MOE_ERR_UNSUPPORTED beyond).
+ *   expert_ids, topk_weights [T, k] int32 / f32, as moe_router_topk writes
+ *            them; an id outside [0, E) sets MOE_DEVERR_EXPERT_ID and its
+ *            slot takes no part; an expert given twice counts twice.
+ *   E, group_offset, num_local_experts: as in moe_sort_by_expert.
+ *   w_format MOE_E4M3FN: w01 [E_loc, 2I, H] (gate rows, then up rows), wo
+ *            [E_loc, H, I] e4m3fn, contraction-contiguous, with f32 scales
+ *            w01_scale [E_loc, kb01, 1, nb01] and wo_scale [E_loc, kbo, 1,
+ *            nbo] under moe_gmm_fp8's rules; H and I multiples of 16.
+ *            MOE_MX4: w01 [E_loc, 2I, H/2], wo [E_loc, H, I/2] codes, e8m0
+ *            scales [E_loc, 2I, H/32] and [E_loc, H, I/32]; kb01 = nb01 = kbo
+ *            = nbo = 0; H and I multiples of 32.
+ *   out      [T, H] bf16 (default) or f32.
+ *   ws       workspace of moe_workspace_bytes(MOE_OP_FFN_TOKENS, T*k, H, I, E),
+ *            zeroed once before its first use; its counters return to zero at
+ *            the end of every call.  Calls that share one must not overlap.
+ * H, I <= 2^20.  w01, wo 16-byte aligned.  Errors: MOE_ERR_SHAPE,
+ * MOE_ERR_UNSUPPORTED, MOE_ERR_NULL, MOE_ERR_WORKSPACE.
+ */
+int moe_ffn_tokens(const void* x, int64_t ldx, const int32_t* expert_ids, const float* topk_weights, int64_t T, int32_t k,
+                   int64_t H, int64_t I, int32_t E, int32_t group_offset, int32_t num_local_experts, int w_format,
+                   const uint8_t* w01, const void* w01_scale, int32_t kb01, int32_t nb01, const uint8_t* wo,
+                   const void* wo_scale, int32_t kbo, int32_t nbo, int out_dtype, void* out, void* ws, size_t ws_bytes,
+                   void* stream);
+
+/*
  * moe_workspace_bytes -- workspace size (host out `bytes`) for `op` with
  * problem sizes d0, d1, d2 and E:
  *   MOE_OP_QUANTIZE_ROWS   d0 = R, d1 = C, d2 = scale_mode
  *   MOE_OP_SORT_BY_EXPERT  d0 = T*k
- *   MOE_OP_GMM, MOE_OP_TGMM d0 = M, d1 = K, d2 = N
+ *   MOE_OP_GMM, MOE_OP_TGMM, MOE_OP_GMM_MX4 d0 = M, d1 = K, d2 = N
+ *   MOE_OP_FFN_TOKENS      d0 = T*k (at most 1024), d1 = H, d2 = I
  *   others                 only the error word
  * Every size is a multiple of 256 bytes and at least 256.
  */

@@ -20,12 +20,13 @@ HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "moe_fp8.h")
 
 # constants mirrored from include/moe_fp8.h
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(6)
-MOE_DTYPE_DEFAULT, MOE_BF16, MOE_F32, MOE_E4M3FN = -1, 0, 1, 2
+MOE_DTYPE_DEFAULT, MOE_BF16, MOE_F32, MOE_E4M3FN, MOE_MX4 = -1, 0, 1, 2, 3
 MOE_SCALE_ROW_DYNAMIC, MOE_SCALE_TENSOR_DYNAMIC, MOE_SCALE_TENSOR_STATIC = 0, 1, 2
 MOE_SCALE_TENSOR_FROM_ROW_AMAX = 3
 MOE_ACT_NONE, MOE_ACT_SILU_MUL = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 (MOE_OP_QUANTIZE_ROWS, MOE_OP_SORT_BY_EXPERT, MOE_OP_GMM, MOE_OP_TGMM, MOE_OP_GATHER_REDUCE,
- MOE_OP_QUANTIZE_WEIGHTS) = range(6)
+ MOE_OP_QUANTIZE_WEIGHTS, MOE_OP_GMM_MX4, MOE_OP_FFN_TOKENS) = range(8)
 MOE_DEVERR_EXPERT_ID, MOE_DEVERR_GROUP_SIZE, MOE_DEVERR_ROWS = 1, 2, 4
 MOE_SORT_NOALLOC_SCRATCH_BYTES = 2 << 20
 
@@ -60,6 +61,17 @@ SIGNATURES = {
     "moe_gather_reduce_backward": (_I, [_P, _P, _P, _P, _I64, ctypes.c_int32, _I64, _P, ctypes.c_int32,
                                         ctypes.c_int32, ctypes.c_int32, _I64, _P, _P, _P, _P, _P, _P]),
     "moe_silu_mul_backward": (_I, [_P, _P, _I64, _P, _I64, _I64, _P, _P, _I64, _P]),
+    "moe_router_topk": (_I, [_P, _I, _I64, _I64, ctypes.c_int32, ctypes.c_int32, _I, _P, _I, _F, _P, _P, _P]),
+    "moe_router_topk_backward": (_I, [_P, _I, _I64, _P, _P, _I64, ctypes.c_int32, ctypes.c_int32, _I, _I, _F, _P, _I64,
+                                      _P]),
+    "moe_quantize_rows_mx4": (_I, [_P, _P, _I64, _I, _I64, _I64, _P, _I64, _P, _I64, _P]),
+    "moe_quantize_weights_mx4": (_I, [_P, _I64, _I64, _I64, _P, _P, _P]),
+    "moe_dequantize_rows_mx4": (_I, [_P, _I64, _P, _I64, _I64, _I64, _I, _P, _I64, _P]),
+    "moe_gmm_mx4": (_I, [_P, _I64, _P, _I64, _I, _I, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _I64,
+                         _I64, _I64, _I, _P, _P, _SZ, _P]),
+    "moe_ffn_tokens": (_I, [_P, _I64, _P, _P, _I64, ctypes.c_int32, _I64, _I64, ctypes.c_int32, ctypes.c_int32,
+                            ctypes.c_int32, _I, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, _P, ctypes.c_int32,
+                            ctypes.c_int32, _I, _P, _P, _SZ, _P]),
     "moe_workspace_bytes": (_I, [_I, _I64, _I64, _I64, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
     "moe_debug_check": (_I, [_P, _P, ctypes.POINTER(ctypes.c_int32)]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
@@ -267,6 +279,54 @@ def moe_silu_mul_backward(a, b, lda, dh, R, C, da, db, ldo, stream=None):
     """a, b, da, db may be column slices of wider buffers (row strides lda, ldo)."""
     return _call("moe_silu_mul_backward", _ptr_rows(a, lda), _ptr_rows(b, lda), lda, _ptr(dh), R, C,
                  _ptr_rows(da, ldo), _ptr_rows(db, ldo), ldo, _stream(stream))
+
+
+def moe_router_topk(logits, logits_dtype, ldl, T, E, k, score, select_bias, renormalize, weight_scale, expert_ids,
+                    topk_weights, stream=None):
+    """logits may be a column slice of a wider buffer (row stride ldl)."""
+    return _call("moe_router_topk", _ptr_rows(logits, ldl), logits_dtype, ldl, T, E, k, score, _ptr(select_bias),
+                 renormalize, float(weight_scale), _ptr(expert_ids), _ptr(topk_weights), _stream(stream))
+
+
+def moe_router_topk_backward(logits, logits_dtype, ldl, expert_ids, dweights, T, E, k, score, renormalize, weight_scale,
+                             dlogits, ldd, stream=None):
+    """logits and dlogits may be column slices of wider buffers (row strides ldl, ldd)."""
+    return _call("moe_router_topk_backward", _ptr_rows(logits, ldl), logits_dtype, ldl, _ptr(expert_ids),
+                 _ptr(dweights), T, E, k, score, renormalize, float(weight_scale), _ptr_rows(dlogits, ldd), ldd,
+                 _stream(stream))
+
+
+def moe_quantize_rows_mx4(x, x_up, ldx, act, R, C, q, ldq, scale, lds, stream=None):
+    """x, x_up, q, scale may be column slices of wider buffers (row strides ldx, ldx, ldq, lds)."""
+    return _call("moe_quantize_rows_mx4", _ptr_rows(x, ldx), _ptr_rows(x_up, ldx), ldx, act, R, C, _ptr_rows(q, ldq), ldq,
+                 _ptr_rows(scale, lds), lds, _stream(stream))
+
+
+def moe_quantize_weights_mx4(w, E, K, N, q, scale, stream=None):
+    return _call("moe_quantize_weights_mx4", _ptr(w), E, K, N, _ptr(q), _ptr(scale), _stream(stream))
+
+
+def moe_dequantize_rows_mx4(q, ldq, scale, lds, R, C, out_dtype, out, ldo, stream=None):
+    """q, scale, out may be column slices of wider buffers (row strides ldq, lds, ldo)."""
+    return _call("moe_dequantize_rows_mx4", _ptr_rows(q, ldq), ldq, _ptr_rows(scale, lds), lds, R, C, out_dtype,
+                 _ptr_rows(out, ldo), ldo, _stream(stream))
+
+
+def moe_gmm_mx4(lhs, ldl, lhs_scale, lds, lhs_format, lhs_scale_mode, rhs, rhs_scale, group_sizes, E, group_offset,
+                num_local_experts, M, K, N, out_dtype, out, ws, stream=None):
+    """lhs, and with MOE_MX4 its scales, may be column slices of wider buffers (row strides ldl, lds)."""
+    ls = _ptr_rows(lhs_scale, lds) if lhs_format == MOE_MX4 else _ptr(lhs_scale)
+    return _call("moe_gmm_mx4", _ptr_rows(lhs, ldl), ldl, ls, lds, lhs_format, lhs_scale_mode, _ptr(rhs), _ptr(rhs_scale),
+                 _ptr(group_sizes), E, group_offset, num_local_experts, M, K, N, out_dtype, _ptr(out), _ptr(ws),
+                 _nbytes(ws), _stream(stream))
+
+
+def moe_ffn_tokens(x, ldx, expert_ids, topk_weights, T, k, H, I, E, group_offset, num_local_experts, w_format, w01,
+                   w01_scale, kb01, nb01, wo, wo_scale, kbo, nbo, out_dtype, out, ws, stream=None):
+    """x may be a column slice of a wider buffer (row stride ldx)."""
+    return _call("moe_ffn_tokens", _ptr_rows(x, ldx), ldx, _ptr(expert_ids), _ptr(topk_weights), T, k, H, I, E,
+                 group_offset, num_local_experts, w_format, _ptr(w01), _ptr(w01_scale), kb01, nb01, _ptr(wo),
+                 _ptr(wo_scale), kbo, nbo, out_dtype, _ptr(out), _ptr(ws), _nbytes(ws), _stream(stream))
 
 
 def moe_debug_check(ws, stream=None):

@@ -1,0 +1,194 @@
+"""GPU parity of the router and its backward against the oracle.
+
+Tolerances (derived, u = 2^-24): a softmax weight is exp(z - m) over a sum.
+z - m is rounded once (|z - m| u on the result's logarithm), expf is within
+2 ulp = 4 u, the sum of up to 1024 positive terms is a 16-term lane sum and a
+6-level tree (each level u) of terms with those errors, and the quotient, the
+renormalisation (the same again) and the factor add u each: a relative
+(2 D + 64) u, D = the largest |z - m| of a chosen expert.  Sigmoid: expf of a
+rounded argument is exact in z, so (64) u.  The gradient's terms carry two
+such weights each: (4 D + 160) u of the sum of the terms' magnitudes, plus
+half a bf16 step (2^-8 of the value) where the result is bf16.  Values below
+2^-120 may lose bits as subnormals: 1e-36 absolute."""
+
+import numpy as np
+import pytest
+import torch
+
+import moe_fp8_grouped_amd as m
+from oracle import router as R
+from tests.parity import dev_f32, dev_i32, host
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+NEG = float(np.finfo(np.float32).min)
+
+CASES = [  # T, E, k, dtype, score, bias, renorm, scale
+    (1, 256, 8, "f32", R.SIGMOID, True, True, 2.5),
+    (1, 1, 1, "f32", R.SOFTMAX, False, True, 1.0),
+    (5, 13, 3, "bf16", R.SOFTMAX, False, False, 1.0),
+    (130, 64, 8, "f32", R.SOFTMAX, False, True, 1.0),
+    (67, 8, 8, "bf16", R.SIGMOID, False, True, 1.5),
+    (33, 1024, 64, "f32", R.SOFTMAX, True, False, 1.0),
+    (257, 72, 6, "bf16", R.SIGMOID, True, False, 2.5),
+    (1000, 256, 8, "bf16", R.SOFTMAX, False, False, 1.0),
+    (259, 128, 4, "f32", R.SOFTMAX, True, True, 0.5),
+    (17, 513, 1, "f32", R.SIGMOID, False, False, 1.0),
+    (4099, 160, 6, "f32", R.SOFTMAX, False, True, 16.0),
+    (3, 65, 2, "bf16", R.SOFTMAX, True, True, 1.0),
+]
+
+
+def draw(T, E, dtype, seed, width=None):
+    """Logits with the rows that matter: masked experts, rows without any
+    expert, the type's lowest value as a mask, equal logits."""
+    rng = np.random.default_rng(seed)
+    z = rng.standard_normal((T, width or E)).astype(np.float32) * 2
+    if T > 2:
+        z[rng.random(z.shape) < 0.05] = -np.inf
+        z[1::7] = -np.inf
+        z[2::11] = NEG
+        z[0, ::2] = NEG
+        z[min(4, T - 1)] = 0.25
+    t = torch.from_numpy(z)
+    if dtype == "bf16":
+        t = t.to(torch.bfloat16)
+    return t.cuda()
+
+
+def run(z, T, E, k, score, bias, renorm, scale, ldl=None):
+    dt = m.MOE_BF16 if z.dtype == torch.bfloat16 else m.MOE_F32
+    ids = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), float("nan"), device="cuda")
+    m.moe_router_topk(z, dt, ldl or E, T, E, k, score, bias, int(renorm), scale, ids, w)
+    return ids, w
+
+
+def span(z, ids):
+    """D: how far below its maximum (or the chosen maximum) a chosen finite logit lies, capped where exp is 0."""
+    zc = np.take_along_axis(z, ids.astype(np.int64), -1)
+    top = np.nanmax(np.where(np.isneginf(z), np.nan, z), axis=-1, initial=-np.inf, keepdims=True)
+    d = np.where(np.isneginf(zc) | np.isneginf(top), 0.0, top - zc)
+    return np.minimum(d, 110.0)
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_topk_matches_the_oracle(case):
+    T, E, k, dtype, score, has_bias, renorm, scale = case
+    z = draw(T, E, dtype, 10 * E + T)
+    bias = np.random.default_rng(E).standard_normal(E).astype(np.float32) * 0.1 if has_bias else None
+    ids, w = run(z, T, E, k, score, None if bias is None else dev_f32(bias), renorm, scale)
+    zf = z.float().cpu().numpy().astype(np.float64)
+    oid, ow = R.router_topk(zf, k, score, bias, renorm, scale)
+    assert (host(ids) == oid).all()
+    tol = (2 * span(zf, oid) * (score == R.SOFTMAX) + 64) * U * np.abs(ow) + 1e-36
+    assert (np.abs(host(w) - ow) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_strided_rows_and_untouched_neighbours(dtype):
+    T, E, k, ld = 37, 40, 4, 56
+    wide = draw(T, E, dtype, 5, width=ld)
+    z = wide[:, 8:8 + E]
+    ids, w = run(z, T, E, k, R.SOFTMAX, None, True, 1.0, ldl=ld)
+    oid, ow = R.router_topk(z.float().cpu().numpy(), k, R.SOFTMAX, None, True)
+    assert (host(ids) == oid).all() and np.allclose(host(w), ow, rtol=2e-5, atol=1e-36)
+    wide_d = torch.full((T, ld), 3.0, dtype=z.dtype, device="cuda")
+    dz = wide_d[:, 8:8 + E]
+    dw = np.random.default_rng(1).standard_normal((T, k)).astype(np.float32)
+    dt = m.MOE_BF16 if dtype == "bf16" else m.MOE_F32
+    m.moe_router_topk_backward(z, dt, ld, ids, dev_f32(dw), T, E, k, R.SOFTMAX, 1, 1.0, dz, ld)
+    assert (wide_d[:, :8] == 3).all() and (wide_d[:, 8 + E:] == 3).all()
+    o, mag = R.router_topk_backward(z.float().cpu().numpy(), oid, dw, R.SOFTMAX, True)
+    assert (np.abs(dz.float().cpu().numpy() - o) <= 1e-4 * mag + 2.0 ** -8 * np.abs(o) + 1e-36).all()
+
+
+def test_nan_logits_are_left_out_and_zero_rows_return():
+    z = torch.tensor([[1.0, float("nan"), 0.5, 2.0], [float("nan")] * 4], device="cuda")
+    ids, w = run(z, 2, 4, 3, R.SOFTMAX, None, False, 1.0)
+    assert host(ids).tolist() == [[3, 0, 2], [0, 1, 2]]
+    assert (host(w)[1] == 0).all() and np.isclose(host(w)[0].sum(), 1.0)
+    empty = torch.empty(0, 4, device="cuda")
+    ids, w = run(empty, 0, 4, 3, R.SOFTMAX, None, False, 1.0)
+    assert ids.numel() == 0
+
+
+BWD = [(1, 256, 8, "f32", R.SIGMOID, True, 2.5), (5, 13, 3, "bf16", R.SOFTMAX, False, 1.0), (130, 64, 8, "f32", R.SOFTMAX, True, 1.0),
+       (67, 8, 8, "bf16", R.SIGMOID, True, 1.5), (9, 1024, 64, "f32", R.SOFTMAX, False, 1.0), (257, 72, 6, "bf16", R.SIGMOID, False, 2.5),
+       (300, 256, 8, "bf16", R.SOFTMAX, True, 1.0), (1, 1, 1, "f32", R.SOFTMAX, False, 1.0), (17, 513, 2, "f32", R.SIGMOID, True, 1.0)]
+
+
+@pytest.mark.parametrize("case", BWD, ids=str)
+def test_backward_matches_the_oracle(case):
+    T, E, k, dtype, score, renorm, scale = case
+    z = draw(T, E, dtype, E + T)
+    ids, _ = run(z, T, E, k, score, None, renorm, scale)
+    ids = host(ids).copy()
+    if T > 3 and k > 1:
+        ids[0, 1] = ids[0, 0]                    # the same expert twice
+        ids[3, 0] = E                            # out of range: takes no part
+    dw = np.random.default_rng(T).standard_normal((T, k)).astype(np.float32)
+    dz = torch.full((T, E), float("nan"), dtype=z.dtype, device="cuda")
+    m.moe_router_topk_backward(z, m.MOE_BF16 if dtype == "bf16" else m.MOE_F32, E, dev_i32(ids), dev_f32(dw), T, E, k, score,
+                               int(renorm), scale, dz, E)
+    zf = z.float().cpu().numpy().astype(np.float64)
+    rows = np.arange(T) != 3 if T > 3 and k > 1 else np.arange(T) >= 0
+    o, mag = R.router_topk_backward(zf[rows], ids[rows], dw[rows], score, renorm, scale)
+    D = span(zf[rows], ids[rows]).max(-1, keepdims=True) * (score == R.SOFTMAX)
+    tol = (4 * D + 160) * U * mag + (2.0 ** -8 * np.abs(o) if dtype == "bf16" else 0) + 1e-36
+    got = dz.float().cpu().numpy()
+    assert (np.abs(got[rows] - o) <= tol).all()
+    assert np.isfinite(got).all()
+    assert (got[np.isneginf(zf)] == 0).all()
+
+
+def test_backward_against_differences():
+    """The float32 forward's own differences at a step where they mean something: weights move by w' h, their
+    rounding is u, so a quotient over 2 h = 2^-5 is off by 2^-24 / 2^-5 and by h^2 / 6 of a third derivative
+    below 1: 2^-10 together with the truncation."""
+    T, E, k = 6, 24, 4
+    z = torch.randn(T, E, generator=torch.Generator().manual_seed(3)).cuda()
+    for score in (R.SOFTMAX, R.SIGMOID):
+        for renorm in (0, 1):
+            ids, _ = run(z, T, E, k, score, None, renorm, 1.0)
+            dw = torch.randn(T, k, generator=torch.Generator().manual_seed(4)).cuda()
+            dz = torch.empty_like(z)
+            m.moe_router_topk_backward(z, m.MOE_F32, E, ids, dw, T, E, k, score, renorm, 1.0, dz, E)
+            base = host(ids)
+            h = 2.0 ** -6
+            for e in range(E):
+                f = []
+                for sgn in (1, -1):
+                    zp = host(z).astype(np.float64)
+                    zp[:, e] += sgn * h
+                    f.append((R.weights_of(zp, base, score, renorm, 1.0) * host(dw)).sum(-1))
+                num = (f[0] - f[1]) / (2 * h)
+                assert np.abs(num - host(dz)[:, e]).max() < 2.0 ** -10
+
+
+def test_other_stream_and_graph():
+    T, E, k = 100, 64, 8
+    z = draw(T, E, "f32", 77)
+    ids, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    dw, dz = torch.ones(T, k, device="cuda"), torch.empty_like(z)
+
+    def step():
+        m.moe_router_topk(z, m.MOE_F32, E, T, E, k, R.SOFTMAX, None, 1, 1.0, ids, w)
+        m.moe_router_topk_backward(z, m.MOE_F32, E, ids, dw, T, E, k, R.SOFTMAX, 1, 1.0, dz, E)
+
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for seed in range(3):
+        z.copy_(draw(T, E, "f32", seed))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        got = [host(v).copy() for v in (ids, w, dz)]
+        step()
+        assert all(np.array_equal(a, host(b)) for a, b in zip(got, (ids, w, dz)))
