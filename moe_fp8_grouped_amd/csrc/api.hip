@@ -7,7 +7,7 @@ size_t quantize_rows_ws_bytes(int64_t R, int64_t C, int mode);
 size_t sort_ws_bytes(int64_t M, int E);
 size_t gmm_ws_bytes();
 size_t tgmm_ws_bytes(int64_t M, int64_t K, int64_t N, int E);
-size_t gmm_mx4_ws_bytes();
+size_t gmm_mx4_ws_bytes(int64_t M, int64_t K);
 size_t ffn_tokens_ws_bytes(int64_t slots, int64_t H, int64_t I);
 }  // namespace moe
 
@@ -31,8 +31,8 @@ extern "C" int moe_workspace_bytes(int op, int64_t d0, int64_t d1, int64_t d2, i
       *bytes = moe::tgmm_ws_bytes(d0, d1, d2, E);
       return MOE_OK;
     case MOE_OP_GMM_MX4:
-      if (d0 < 0 || d1 < 0 || d2 < 0) return MOE_ERR_SHAPE;
-      *bytes = moe::gmm_mx4_ws_bytes();
+      if (d0 < 0 || d1 < 0 || d2 < 0 || d0 > INT32_MAX || d1 > (1 << 22)) return MOE_ERR_SHAPE;
+      *bytes = moe::gmm_mx4_ws_bytes(d0, d1);
       return MOE_OK;
     case MOE_OP_FFN_TOKENS:
       if (d0 < 0 || d0 > 1024 || d1 < 0 || d1 > (1 << 20) || d2 < 0 || d2 > (1 << 20)) return MOE_ERR_SHAPE;

@@ -271,3 +271,43 @@ def test_gmm_bad_groups_are_flagged_and_stay_inside(K, N):
     g, err = run_gmm(dev_u8(lq), dev_u8(lsc), m.MOE_MX4, m.MOE_SCALE_ROW_DYNAMIC, dev_u8(q), dev_u8(s), np.array([4, 5, 6], np.int32), 3, 1, 0,
                      M, K, N, m.MOE_BF16)
     assert err == 0 and (g == 0).all()
+
+
+@pytest.mark.parametrize("K,N", [(1312, 2064), (2304, 2048), (160, 2320), (32, 2064)])
+@pytest.mark.parametrize("fmt", [m.MOE_E4M3FN, m.MOE_MX4])
+def test_gmm_enough_tiles_for_the_wide_kernel(K, N, fmt):
+    """64 groups by nine column tiles: the 256-column tiles, with every row count a tile may have.  Codes are drawn
+    (any code, scales of 2^-12 .. 1), so the products' exponents are spread over the formats."""
+    rng = np.random.default_rng([K, N, fmt])
+    El = 64
+    gs = rng.choice([0, 1, 3, 16, 17, 31, 33], El).astype(np.int32)
+    gs[[5, 20, 40, 41, 63]] = [64, 65, 97, 128, 150]
+    gs[[0, 1, 2, 62]] = [0, 1, 16, 0]
+    n = int(gs.sum())
+    M = n + 5
+    q = rng.integers(0, 256, (El, N, K // 2), dtype=np.uint8)
+    s = rng.integers(115, 128, (El, N, K // 32), dtype=np.uint8)
+    if fmt == m.MOE_E4M3FN:
+        lhs, ls, _ = quantize_rows(bits(rng, M, K), SCALE_ROW_DYNAMIC)
+        dl, ds = dev_u8(lhs), dev_f32(ls)
+        X = e4m3_decode(lhs) * ls.astype(np.float64)[:, None]
+    else:
+        lhs, ls = mx4.quantize_rows_mx4(bits(rng, M, K))
+        dl, ds = dev_u8(lhs), dev_u8(ls)
+    o, A = mx4.gmm_mx4(lhs, ls, q, s, gs, 0, El, M)
+    offs = np.concatenate([[0], np.cumsum(gs)])
+
+    def B(idx):
+        out = np.zeros(len(idx))
+        for i, (rr, cc) in enumerate(zip(idx // N, idx % N)):
+            g = int(np.searchsorted(offs[1:], rr, side="right"))
+            if g < El:
+                out[i] = allowance(X[rr:rr + 1], lhs[rr:rr + 1], mx4.decode(q[g][cc:cc + 1], s[g][cc:cc + 1]),
+                                   mx4.unpack(q[g][cc:cc + 1]))[0, 0]
+        return out
+    dq, dsw = dev_u8(q), dev_u8(s)
+    for dtype in (m.MOE_F32, m.MOE_BF16):
+        g, err = run_gmm(dl, ds, fmt, m.MOE_SCALE_ROW_DYNAMIC, dq, dsw, gs, El, 0, El, M, K, N, dtype)
+        assert err == 0
+        (check_f32 if dtype == m.MOE_F32 else check_bf16)(g, o, A, "wide", hw_allowance=B if fmt == m.MOE_E4M3FN else None)
+        assert (g[n:] == 0).all()
