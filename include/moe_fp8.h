@@ -653,8 +653,12 @@ int moe_dequantize_rows_mx4(const uint8_t* q, int64_t ldq, const uint8_t* scale,
  *            (moe_quantize_weights_mx4).
  *   group_sizes .. num_local_experts, out, out_dtype as in moe_gmm_fp8.
  *   ws       workspace of moe_workspace_bytes(MOE_OP_GMM_MX4, M, K, N, E).
- * K a multiple of 32, N of 16, ldl a multiple of 16 and at least a row's
- * bytes; lhs, rhs, out 16-byte aligned.  Errors as in moe_gmm_fp8.
+ *            Scale rows of a 4-bit lhs that are not dword aligned (lds, or
+ *            lhs_scale itself) are copied there first; calls that may overlap
+ *            need a workspace each.
+ * K a multiple of 32 and at most 2^22, N of 16, N * K / 32 below 2^31, ldl a
+ * multiple of 16, at least a row's bytes and at most 2^23; lhs, rhs, rhs_scale,
+ * out 16-byte aligned.  Errors as in moe_gmm_fp8.
  */
 int moe_gmm_mx4(const uint8_t* lhs, int64_t ldl, const void* lhs_scale, int64_t lds, int lhs_format,
                 int lhs_scale_mode, const uint8_t* rhs, const uint8_t* rhs_scale, const int32_t* group_sizes, int32_t E,
