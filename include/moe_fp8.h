@@ -689,9 +689,9 @@ int moe_gmm_mx4(const uint8_t* lhs, int64_t ldl, const void* lhs_scale, int64_t 
  *            = nbo = 0; H and I multiples of 32.
  *   out      [T, H] bf16 (default) or f32.
  *   ws       workspace of moe_workspace_bytes(MOE_OP_FFN_TOKENS, T*k, H, I, E),
- *            zeroed once before its first use; its counters return to zero at
- *            the end of every call.  Calls that share one must not overlap.
- * H, I <= 2^20.  w01, wo 16-byte aligned.  Errors: MOE_ERR_SHAPE,
+ *            zeroed once before its first use (the error word).  Calls that
+ *            share one must not overlap.
+ * H, I <= 2^20.  w01, wo, out 16-byte aligned, the scales 4-byte.  Errors: MOE_ERR_SHAPE,
  * MOE_ERR_UNSUPPORTED, MOE_ERR_NULL, MOE_ERR_WORKSPACE.
  */
 int moe_ffn_tokens(const void* x, int64_t ldx, const int32_t* expert_ids, const float* topk_weights, int64_t T, int32_t k,

@@ -21,8 +21,8 @@
 //   e4m3 rows, 128 x 256 tiles (run_tile, 4 column fragments a wave): 32768
 //     rows of 2048 by 64 groups of 1536 columns 132 us, 1.55 PFLOP/s (as
 //     256 x 256 tiles with the weights through LDS: 142).
-//   fewer rows, 64-column tiles (run_tile, one column fragment a wave): some
-//     80 us with the wide tiles become 18 on the smallest products.
+//   fewer tiles than workgroups: 64-column tiles (run_tile, one column
+//     fragment a wave).
 #include <type_traits>
 
 #include "mx4_common.hpp"
