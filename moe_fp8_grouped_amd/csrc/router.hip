@@ -25,7 +25,7 @@ __device__ __forceinline__ float load_logit(const void* z, int64_t i) {
 __device__ __forceinline__ float masked(float z) { return z != z ? -INFINITY : z; }
 
 // Monotone unsigned keys: a larger key is a larger value; 0 is below all.
-__device__ __forceinline__ uint64_t order_key(float z) {
+__device__ __forceinline__ uint32_t order_key(float z) {
   const uint32_t b = __float_as_uint(z + 0.0f);             // -0 and +0 are equal keys
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
@@ -34,7 +34,59 @@ __device__ __forceinline__ uint64_t order_key(double v) {
   return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
 }
 
-// One wave per row, expert e = lane + 64 i in register i.
+// Reductions over the wave, the same value for every lane: rows of 16 by shifts,
+// then rows into rows, all in the vector unit (through LDS, as a shuffle goes,
+// the k dependent reductions of the choice took most of the kernel's time).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t none, uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(none), static_cast<int>(v), CTRL, ROWS, 0xf, false));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float none, float v) {
+  return __uint_as_float(dpp<CTRL, ROWS>(__float_as_uint(none), __float_as_uint(v)));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double none, double v) {
+  const uint64_t n = __double_as_longlong(none), b = __double_as_longlong(v);
+  const uint32_t lo = dpp<CTRL, ROWS>(static_cast<uint32_t>(n), static_cast<uint32_t>(b));
+  const uint32_t hi = dpp<CTRL, ROWS>(static_cast<uint32_t>(n >> 32), static_cast<uint32_t>(b >> 32));
+  return __longlong_as_double(static_cast<int64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane) {
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane));
+}
+__device__ __forceinline__ float from_lane(float v, int lane) { return __uint_as_float(from_lane(__float_as_uint(v), lane)); }
+__device__ __forceinline__ double from_lane(double v, int lane) {
+  const uint64_t b = __double_as_longlong(v);
+  const uint32_t lo = from_lane(static_cast<uint32_t>(b), lane), hi = from_lane(static_cast<uint32_t>(b >> 32), lane);
+  return __longlong_as_double(static_cast<int64_t>(hi) << 32 | lo);
+}
+template <class T, class F>
+__device__ __forceinline__ T over_wave(T v, T none, const F& f) {
+  v = f(v, dpp<0x111, 0xf>(none, v));        // row_shr 1, 2, 4, 8
+  v = f(v, dpp<0x112, 0xf>(none, v));
+  v = f(v, dpp<0x114, 0xf>(none, v));
+  v = f(v, dpp<0x118, 0xf>(none, v));
+  v = f(v, dpp<0x142, 0xa>(none, v));        // row_bcast 15 into rows 1 and 3, 31 into rows 2 and 3
+  v = f(v, dpp<0x143, 0xc>(none, v));
+  return from_lane(v, 63);
+}
+template <class T>
+__device__ __forceinline__ T sum_of(T v) {
+  return over_wave(v, T(0), [](T a, T b) { return a + b; });
+}
+__device__ __forceinline__ float max_of(float v) {
+  return over_wave(v, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ uint32_t max_of(uint32_t v) {
+  return over_wave(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+
+// One wave per row, expert e = lane + 64 i in register i.  Every choice is one
+// maximum over the wave (two for the bias's 64-bit keys), and ballots that find
+// its first expert.  8192 rows of 256 bf16 logits, k = 8: 10.2 us (with every
+// choice through LDS shuffles of key, expert and logit 25); what is left is
+// instructions, not the 0.9 us of bytes.
 template <bool BF16, int V, bool BIAS, bool SIGMOID>
 __global__ __launch_bounds__(256) void router_topk_kernel(const void* __restrict__ logits, int64_t ldl, int64_t T, int E,
                                                           int k, const float* __restrict__ bias, int renorm, float scale,
@@ -51,7 +103,7 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const void* __restrict
   float m = z[0];
 #pragma unroll
   for (int i = 1; i < V; ++i) m = fmaxf(m, z[i]);
-  m = wave_max(m);
+  m = max_of(m);
   const float m0 = m == -INFINITY ? 0.0f : m;
   // softmax's denominator (64-bit where a bias is added to the scores)
   float sum = 0.0f;
@@ -66,58 +118,64 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const void* __restrict
       }
       sum += expf(z[i] - m0);
     }
-    sum = wave_sum(sum);
-    if constexpr (BIAS) {
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) dsum += __shfl_xor(dsum, o, MOE_WAVE);
-    }
+    sum = sum_of(sum);
+    if constexpr (BIAS) dsum = sum_of(dsum);
   }
-  uint64_t key[V];
+  // keys by halves; without a bias the upper one says all
+  uint32_t hi[V], lo[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = lane + 64 * i;
+    uint64_t key;
     if constexpr (BIAS) {
       const double s = SIGMOID ? 1.0 / (1.0 + exp(-static_cast<double>(z[i]))) : p[i] / dsum;
       const bool in = z[i] > -INFINITY;
-      key[i] = e >= E ? 0 : order_key(in ? s + static_cast<double>(bias[e < E ? e : 0]) : -static_cast<double>(INFINITY));
+      key = order_key(in ? s + static_cast<double>(bias[e < E ? e : 0]) : -static_cast<double>(INFINITY));
     } else {
-      key[i] = e >= E ? 0 : order_key(z[i]);
+      key = static_cast<uint64_t>(order_key(z[i])) << 32;
     }
+    hi[i] = e < E ? static_cast<uint32_t>(key >> 32) : 0;   // (0 is below every expert's)
+    lo[i] = static_cast<uint32_t>(key);
   }
   float my_z = -INFINITY;                    // lane j: the j-th choice
   int my_id = 0;
   for (int j = 0; j < k; ++j) {
-    uint64_t bk = 0;
-    int bi = kMaxE;
-    float bz = -INFINITY;
+    uint32_t top = hi[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (key[i] > bk) { bk = key[i]; bi = lane + 64 * i; bz = z[i]; }
+    for (int i = 1; i < V; ++i) top = max(top, hi[i]);
+    top = max_of(top);
+    uint32_t low = 0;
+    if constexpr (BIAS) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) low = max(low, hi[i] == top ? lo[i] : 0u);
+      low = max_of(low);
     }
+    bool found = false;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      const uint64_t ok = __shfl_xor(bk, o, MOE_WAVE);
-      const int oi = __shfl_xor(bi, o, MOE_WAVE);
-      const float oz = __shfl_xor(bz, o, MOE_WAVE);
-      if (ok > bk || (ok == bk && oi < bi)) { bk = ok; bi = oi; bz = oz; }
+    for (int i = 0; i < V; ++i) {            // experts in order
+      const uint64_t at = __ballot(hi[i] == top && (!BIAS || lo[i] == low));
+      if (!found && at) {
+        found = true;
+        const int l = __builtin_ctzll(at);
+        if (lane == j) my_id = l + 64 * i;
+        const float zl = from_lane(z[i], l);
+        if (lane == j) my_z = zl;
+        if (lane == l) hi[i] = 0;
+      }
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (bi == lane + 64 * i) key[i] = 0;
-    if (lane == j) { my_z = bz; my_id = bi; }
   }
   float w;
   if (SIGMOID) {
     w = 1.0f / (1.0f + expf(-my_z));
   } else {
-    const float top = wave_max(my_z);        // renormalised softmax: a softmax over the chosen
+    const float top = max_of(my_z);        // renormalised softmax: a softmax over the chosen
     const float base = renorm ? (top == -INFINITY ? 0.0f : top) : m0;
     w = expf(my_z - base);
     if (!renorm) w = sum > 0.0f ? w / sum : 0.0f;
   }
   if (lane >= k) w = 0.0f;
   if (renorm) {
-    const float tot = wave_sum(w);
+    const float tot = sum_of(w);
     w = tot > 0.0f ? w / tot : 0.0f;
   }
   if (lane < k) {
@@ -152,8 +210,8 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(const void* __restrict_
   const int id_l = lane < k ? ids[t * k + lane] : -1;
   const float dw_l = lane < k ? dweights[t * k + lane] * scale : 0.0f;
   for (int j = 0; j < k; ++j) {
-    const int id = __shfl(id_l, j, MOE_WAVE);
-    const float dw = __shfl(dw_l, j, MOE_WAVE);
+    const int id = __builtin_amdgcn_readlane(id_l, j);
+    const float dw = from_lane(dw_l, j);
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (id == lane + 64 * i && id < E) { g[i] += dw; n[i] += 1.0f; }
@@ -161,7 +219,7 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(const void* __restrict_
   float m = -INFINITY;                       // over all experts, or the chosen ones
 #pragma unroll
   for (int i = 0; i < V; ++i) m = fmaxf(m, (!renorm || n[i] > 0.0f) ? z[i] : -INFINITY);
-  m = wave_max(m);
+  m = max_of(m);
   const float m0 = m == -INFINITY ? 0.0f : m;
   float p[V], sum = 0.0f, dot = 0.0f;
 #pragma unroll
@@ -175,8 +233,8 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(const void* __restrict_
     }
     dot += g[i] * p[i];
   }
-  sum = wave_sum(sum);
-  dot = wave_sum(dot);
+  sum = sum_of(sum);
+  dot = sum_of(dot);
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
