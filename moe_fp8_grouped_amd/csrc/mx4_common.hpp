@@ -27,26 +27,6 @@ __device__ __forceinline__ float scale_value(uint32_t code) {
   return __uint_as_float(code == 0u ? 0x00400000u : code == 255u ? 0x7fc00000u : code << 23);
 }
 
-// Its reciprocal 2^(127 - code), exact; a NaN block multiplies by 0, so its
-// codes are 0 (NaN and infinities included: encode() takes NaN to 0).
-__device__ __forceinline__ float scale_inverse(uint32_t code) {
-  return code == 255u ? 0.0f : __uint_as_float((254u - code) << 23);
-}
-
-// Nearest e2m1 code, ties to the even code, saturating at 6; NaN gives 0.
-__device__ __forceinline__ uint32_t encode(float v) {
-  const float a = fabsf(v);
-  uint32_t c = 0;
-  c += a > 0.25f;
-  c += a >= 0.75f;
-  c += a > 1.25f;
-  c += a >= 1.75f;
-  c += a > 2.5f;
-  c += a >= 3.5f;
-  c += a > 5.0f;
-  return c | (a == a ? (__float_as_uint(v) >> 28) & 8u : 0u);
-}
-
 __device__ __forceinline__ float decode(uint32_t c) {
   const uint32_t e = (c >> 1) & 3u, f = c & 1u;
   const float a = e == 0 ? 0.5f * static_cast<float>(f)
