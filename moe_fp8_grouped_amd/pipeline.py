@@ -9,6 +9,10 @@ review comments): quantize tokens -> sort/gather fp8 rows -> gmm(s) ->
 ("Support quantization for tokamax gmm v2", gmm2 / tgmm2): dX = gmm(dY,
 W^T) and dW = tgmm(X, dY).
 
+RoutedFFN starts at the router's logits, with 4-bit expert weights: router ->
+the steps above over the microscaled 4-bit format -> gather-reduce, or, for a
+few tokens, router -> the whole layer in one call; and the router's gradient.
+
 Expert parallelism is modelled as one GPU's slice: experts
 [group_offset, group_offset + num_local_experts) are local; the sorted
 buffers hold only their rows (compact window).  With ``share`` the step
@@ -20,11 +24,13 @@ are quantized once at setup.
 import numpy as np
 import torch
 
-from . import (MOE_ACT_NONE, MOE_ACT_SILU_MUL, MOE_BF16, MOE_E4M3FN, MOE_F32, MOE_OP_GATHER_REDUCE, MOE_OP_GMM,
-               MOE_OP_QUANTIZE_ROWS, MOE_OP_SORT_BY_EXPERT, MOE_OP_TGMM, MOE_SCALE_ROW_DYNAMIC, MOE_SCALE_TENSOR_DYNAMIC,
-               MOE_SCALE_TENSOR_FROM_ROW_AMAX, MOE_SCALE_TENSOR_STATIC, moe_gather_reduce, moe_gather_reduce_backward,
-               moe_gmm_fp8, moe_quantize_rows, moe_quantize_rows_strided, moe_quantize_sort_by_expert,
-               moe_quantize_weights, moe_silu_mul_backward, moe_sort_by_expert, moe_sort_gather_transposed,
+from . import (MOE_ACT_NONE, MOE_ACT_SILU_MUL, MOE_BF16, MOE_E4M3FN, MOE_F32, MOE_MX4, MOE_OP_FFN_TOKENS,
+               MOE_OP_GATHER_REDUCE, MOE_OP_GMM, MOE_OP_GMM_MX4, MOE_OP_QUANTIZE_ROWS, MOE_OP_SORT_BY_EXPERT, MOE_OP_TGMM,
+               MOE_SCALE_ROW_DYNAMIC, MOE_SCALE_TENSOR_DYNAMIC, MOE_SCALE_TENSOR_FROM_ROW_AMAX, MOE_SCALE_TENSOR_STATIC,
+               MOE_SCORE_SOFTMAX, moe_ffn_tokens, moe_gather_reduce, moe_gather_reduce_backward, moe_gmm_fp8,
+               moe_gmm_mx4, moe_quantize_rows, moe_quantize_rows_mx4, moe_quantize_rows_strided,
+               moe_quantize_sort_by_expert, moe_quantize_weights, moe_quantize_weights_mx4, moe_router_topk,
+               moe_router_topk_backward, moe_silu_mul_backward, moe_sort_by_expert, moe_sort_gather_transposed,
                moe_tgmm_fp8, moe_tgmm_fp8_xt, tgmm_xt_cols, workspace)
 
 
@@ -512,6 +518,175 @@ class FFNBackwardPath:
     def capture_graph(self, warmup=1):
         """Record one backward step into a HIP graph (every buffer it writes is
         fully rewritten by it, so replays equal eager steps)."""
+        for _ in range(warmup):
+            self.step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            self.step()
+        torch.cuda.synchronize()
+        self.graph = g
+        return g
+
+    def replay(self):
+        self.graph.replay()
+
+
+class MxWeight:
+    """An expert weight [E, K, N] bf16 in the microscaled 4-bit format, blocks
+    along K: codes [E, N, K/2], scales [E, N, K/32]."""
+
+    def __init__(self, w_bf16: torch.Tensor, stream=None):
+        self.E, self.K, self.N = w_bf16.shape
+        self.q = torch.empty((self.E, self.N, self.K // 2), dtype=torch.uint8, device=w_bf16.device)
+        self.scale = torch.empty((self.E, self.N, self.K // 32), dtype=torch.uint8, device=w_bf16.device)
+        moe_quantize_weights_mx4(w_bf16, self.E, self.K, self.N, self.q, self.scale, stream=stream)
+
+
+class MxRows:
+    """4-bit rows [R, C], codes and scales as parts of one row, so that one
+    gather moves both."""
+
+    def __init__(self, R, C, device):
+        self.C, self.ld = C, -(-(C // 2 + C // 32) // 16) * 16
+        self.rows = torch.zeros((R, self.ld), dtype=torch.uint8, device=device)
+        self.q, self.scale = self.rows[:, :C // 2], self.rows[:, C // 2:]
+
+    def quantize(self, x, x_up, ldx, act, R):
+        moe_quantize_rows_mx4(x, x_up, ldx, act, R, self.C, self.q, self.ld, self.scale, self.ld)
+
+
+class RoutedFFN:
+    """The gated expert layer of ``T`` tokens from the router's logits [T, E],
+    expert weights in the 4-bit format:
+
+      router    ids, weights = top-k of the logits
+      few       out = the whole layer in one call, tokens unquantized
+                (up to 64 tokens and 1024 routed rows)
+      otherwise x to rows (4-bit, or e4m3 with a scale a row) -> sort ->
+                [a | b] = gmm -> SiLU*mul to rows -> gmm -> gather-reduce
+
+    ``w0``, ``w1`` [E_loc, H, I] and ``wo`` [E_loc, I, H] bf16 are quantized
+    here, once.  ``x`` [T, H] bf16 and ``logits`` [T, E] (bf16 or f32) are
+    the buffers a step reads.  router_backward() gives the gradient of the
+    logits after a step that kept the experts' outputs (not ``few``)."""
+
+    FEW_TOKENS, FEW_ROWS = 64, 1024
+
+    def __init__(self, x, logits, w0, w1, wo, k, rows=MOE_MX4, few=None, score=MOE_SCORE_SOFTMAX, renormalize=True,
+                 weight_scale=1.0, select_bias=None, group_offset=0, m_cap=None):
+        dev = x.device
+        self.x, self.logits, self.k, self.rows = x, logits, k, rows
+        self.T, self.H = x.shape
+        self.E, self.El, self.g0 = logits.shape[1], w0.shape[0], group_offset
+        self.I = I = w0.shape[2]
+        T, H, E, El = self.T, self.H, self.E, self.El
+        if rows not in (MOE_MX4, MOE_E4M3FN):
+            raise ValueError("rows must be MOE_MX4 or MOE_E4M3FN")
+        fits = T <= self.FEW_TOKENS and T * k <= self.FEW_ROWS
+        if few and not fits:
+            raise ValueError("the few-token layer takes up to 64 tokens and 1024 routed rows")
+        self.few = fits if few is None else bool(few)
+        self.logits_dtype = MOE_BF16 if logits.dtype == torch.bfloat16 else MOE_F32
+        self.routing = (score, int(renormalize), float(weight_scale))
+        self.bias = select_bias
+        u8, f32, i32, bf = torch.uint8, torch.float32, torch.int32, torch.bfloat16
+        self.w01 = MxWeight(torch.cat([w0, w1], dim=2).contiguous())
+        self.wo = MxWeight(wo)
+        self.ids = torch.empty((T, k), dtype=i32, device=dev)
+        self.topk_w = torch.empty((T, k), dtype=f32, device=dev)
+        self.out = torch.empty((T, H), dtype=bf, device=dev)
+        if self.few:
+            self.ws = workspace(MOE_OP_FFN_TOKENS, T * k, H, I, E, device=dev)
+            return
+        self.M = M = T * k
+        self.m_cap = Mc = M if m_cap is None else m_cap
+        self.perm = torch.empty(M, dtype=i32, device=dev)
+        self.inv_pos = torch.empty(M, dtype=i32, device=dev)
+        self.group_sizes = torch.empty(E, dtype=i32, device=dev)
+        if rows == MOE_MX4:
+            self.xq, self.xs, self.hq = MxRows(T, H, dev), MxRows(Mc, H, dev), MxRows(Mc, I, dev)
+            self.one = torch.ones((1,), dtype=f32, device=dev)
+        else:
+            self.xs = torch.empty((Mc, H), dtype=u8, device=dev)
+            self.ss = torch.empty((Mc,), dtype=f32, device=dev)
+            self.hq = torch.empty((Mc, I), dtype=u8, device=dev)
+            self.hs = torch.empty((Mc,), dtype=f32, device=dev)
+        self.ab = torch.empty((Mc, 2 * I), dtype=bf, device=dev)
+        self.y = torch.empty((Mc, H), dtype=bf, device=dev)
+        self.ws_sort = workspace(MOE_OP_SORT_BY_EXPERT, M, 0, 0, E, device=dev)
+        self.ws_up = workspace(MOE_OP_GMM_MX4, Mc, H, 2 * I, E, device=dev)
+        self.ws_down = workspace(MOE_OP_GMM_MX4, Mc, I, H, E, device=dev)
+
+    # -- steps -------------------------------------------------------------
+    def route(self):
+        moe_router_topk(self.logits, self.logits_dtype, self.E, self.T, self.E, self.k, self.routing[0], self.bias,
+                        self.routing[1], self.routing[2], self.ids, self.topk_w)
+
+    def sort(self):
+        T, H, k, E = self.T, self.H, self.k, self.E
+        if self.rows == MOE_MX4:
+            self.xq.quantize(self.x, None, H, MOE_ACT_NONE, T)
+            moe_sort_by_expert(self.ids, T, k, E, self.g0, self.El, self.xq.rows, self.one, MOE_SCALE_TENSOR_STATIC,
+                               self.xq.ld, self.m_cap, self.perm, self.inv_pos, self.group_sizes, self.xs.rows, None,
+                               self.ws_sort)
+        else:
+            moe_quantize_sort_by_expert(self.x, T, H, MOE_SCALE_ROW_DYNAMIC, 0.0, self.ids, k, E, self.g0, self.El,
+                                        self.m_cap, self.perm, self.inv_pos, self.group_sizes, self.xs, self.ss, None,
+                                        self.ws_sort)
+
+    def _gmm(self, lhs, ls, w: MxWeight, out, ws):
+        if self.rows == MOE_MX4:
+            a = (lhs.q, lhs.ld, lhs.scale, lhs.ld)
+        else:
+            a = (lhs, w.K, ls, 0)
+        moe_gmm_mx4(*a, self.rows, MOE_SCALE_ROW_DYNAMIC, w.q, w.scale, self.group_sizes, self.E, self.g0, self.El,
+                    self.m_cap, w.K, w.N, MOE_BF16, out, ws)
+
+    def experts(self):
+        I, mx = self.I, self.rows == MOE_MX4
+        self._gmm(self.xs, None if mx else self.ss, self.w01, self.ab, self.ws_up)
+        a, b = self.ab[:, :I], self.ab[:, I:]
+        if mx:
+            self.hq.quantize(a, b, 2 * I, MOE_ACT_SILU_MUL, self.m_cap)
+        else:
+            moe_quantize_rows_strided(a, b, 2 * I, MOE_ACT_SILU_MUL, self.m_cap, I, MOE_SCALE_ROW_DYNAMIC, 0.0, self.hq,
+                                      self.hs)
+        self._gmm(self.hq, None if mx else self.hs, self.wo, self.y, self.ws_down)
+
+    def combine(self):
+        moe_gather_reduce(self.y, MOE_BF16, self.inv_pos, self.topk_w, self.T, self.k, self.H, MOE_BF16, self.out)
+
+    def step(self):
+        self.route()
+        if self.few:
+            moe_ffn_tokens(self.x, self.H, self.ids, self.topk_w, self.T, self.k, self.H, self.I, self.E, self.g0, self.El,
+                           MOE_MX4, self.w01.q, self.w01.scale, 0, 0, self.wo.q, self.wo.scale, 0, 0, MOE_BF16, self.out,
+                           self.ws)
+            return
+        self.sort()
+        self.experts()
+        self.combine()
+
+    def router_backward(self, dout):
+        """dout [T, H] bf16, the gradient of ``out`` -> dlogits, through the
+        routing weights (the experts' own gradients are not formed here);
+        also ``dy`` [m_cap, H], the sorted rows' gradient, and ``dw`` [T, k]."""
+        if self.few:
+            raise ValueError("the few-token layer keeps no expert outputs: build the layer with few=False")
+        if not hasattr(self, "dlogits"):
+            self.dy = torch.empty((self.m_cap, self.H), dtype=torch.bfloat16, device=dout.device)
+            self.dw = torch.empty((self.T, self.k), dtype=torch.float32, device=dout.device)
+            self.dlogits = torch.empty_like(self.logits)
+        moe_gather_reduce_backward(dout, self.y, self.inv_pos, self.topk_w, self.T, self.k, self.H, self.group_sizes,
+                                   self.E, self.g0, self.El, self.m_cap, self.dy, self.dw, None, None, None)
+        moe_router_topk_backward(self.logits, self.logits_dtype, self.E, self.ids, self.dw, self.T, self.E, self.k,
+                                 self.routing[0], self.routing[1], self.routing[2], self.dlogits, self.E)
+
+    # -- HIP graph of one step ------------------------------------------------
+    def capture_graph(self, warmup=2):
+        """Record one step into a HIP graph (every buffer it writes is fully
+        rewritten by it, so replays equal eager steps)."""
         for _ in range(warmup):
             self.step()
         torch.cuda.synchronize()

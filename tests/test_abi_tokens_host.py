@@ -110,3 +110,15 @@ def test_workspace_sizes(lib):
     for bad in ((1025, 512, 256), (8, -1, 256), (8, 512, (1 << 20) + 1)):
         with pytest.raises(m.MoeError):
             m.workspace_bytes(m.MOE_OP_FFN_TOKENS, *bad, 8)
+
+
+def test_alignment_of_what_is_loaded_wide(lib):
+    """Scales, and the results that leave in whole vectors."""
+    def g(rs=AL, fmt=m.MOE_MX4):
+        return lib.moe_gmm_mx4(AL, 32, AL, 2, fmt, 0, AL, rs, AL, 8, 0, 8, 16, 64, 32, 0, AL, AL, 1 << 30, None)
+
+    def f(s01=AL, so=AL, out=AL):
+        return lib.moe_ffn_tokens(AL, 256, AL, AL, 4, 2, 256, 128, 8, 0, 8, m.MOE_MX4, AL, s01, 0, 0, AL, so, 0, 0, 0, out, AL, 1 << 30, None)
+    assert g(rs=AL + 4) == m.MOE_ERR_SHAPE
+    for bad in (dict(s01=AL + 2), dict(so=AL + 1), dict(out=AL + 8)):
+        assert f(**bad) == m.MOE_ERR_SHAPE, bad

@@ -201,3 +201,17 @@ def test_streams_graph_replays_and_a_shared_workspace():
         step()
         assert all(np.array_equal(a, host(b)) for a, b in zip(got, (mid, out)))
     assert m.moe_debug_check(ws) == 0
+
+
+LONG = [  # rows and weights beyond what a workgroup stages or takes at once
+    ("mx4", 20, 2, 2, 0, 2, 2336, 1120, None, None),          # 20 slots an expert, both contractions in parts, short last chunks
+    ("e4m3", 20, 2, 2, 0, 2, 2352, 1040, (1, 1), None),
+    ("e4m3", 3, 4, 8, 0, 8, 48, 4112, (1, 1), None),          # several units a wave, some left over
+    ("mx4", 5, 8, 8, 0, 8, 8224, 64, None, None),             # the first contraction in parts, many output columns
+    ("e4m3", 17, 4, 4, 0, 4, 2080, 4112, (1, 1), None),       # parts, passes and a wave's own units together
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=str)
+def test_long_rows_and_many_units(case):
+    test_matches_the_oracle(case)
