@@ -531,8 +531,7 @@ __global__ __launch_bounds__(kThreads) void ffn_combine_kernel(const FfnArgs p) 
         in[j] = j0 + j < p.k && id >= 0 && id < p.E && id >= p.g0 && id < p.g0 + p.El;
         w[j] = p.tw[s];
         if (c == 0 && (id < 0 || id >= p.E)) raise_error(p.err, MOE_DEVERR_EXPERT_ID);
-        y[j] = v4f{0.f, 0.f, 0.f, 0.f};
-        if (in[j]) y[j] = *reinterpret_cast<const v4f*>(p.y + static_cast<int64_t>(s) * p.H + c);
+        y[j] = *reinterpret_cast<const v4f*>(p.y + static_cast<int64_t>(s) * p.H + c);     // (unused where no expert wrote it)
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
