@@ -192,3 +192,20 @@ def test_other_stream_and_graph():
         got = [host(v).copy() for v in (ids, w, dz)]
         step()
         assert all(np.array_equal(a, host(b)) for a, b in zip(got, (ids, w, dz)))
+
+
+def test_tensors_and_streams_of_another_device_are_refused(monkeypatch):
+    z, ids, w = torch.zeros(2, 8, device="cuda"), torch.zeros(2, 2, dtype=torch.int32, device="cuda"), torch.zeros(2, 2, device="cuda")
+    st = torch.cuda.Stream()
+    args = (z, m.MOE_F32, 8, 2, 8, 2, R.SOFTMAX, None, 1, 1.0, ids, w)
+    m.moe_router_topk(*args, stream=st)
+    torch.cuda.synchronize()
+    monkeypatch.setattr(m, "_current_device", lambda: z.get_device() + 1)
+    for stream in (None, st):
+        with pytest.raises(ValueError):
+            m.moe_router_topk(*args, stream=stream)
+    with pytest.raises(ValueError):
+        m._stream_here(st)
+    with pytest.raises(ValueError):
+        m.moe_quantize_weights_mx4(torch.zeros(1, 32, 16, dtype=torch.bfloat16, device="cuda"), 1, 32, 16,
+                                   torch.zeros(1, 16, 16, dtype=torch.uint8, device="cuda"), torch.zeros(1, 16, 1, dtype=torch.uint8, device="cuda"))
