@@ -209,3 +209,23 @@ def test_tensors_and_streams_of_another_device_are_refused(monkeypatch):
     with pytest.raises(ValueError):
         m.moe_quantize_weights_mx4(torch.zeros(1, 32, 16, dtype=torch.bfloat16, device="cuda"), 1, 32, 16,
                                    torch.zeros(1, 16, 16, dtype=torch.uint8, device="cuda"), torch.zeros(1, 16, 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("T,E,k,dtype,ldl,ldd", [(40, 100, 33, "f32", 100, 104), (19, 64, 64, "bf16", 67, 64), (21, 128, 17, "bf16", 132, 136),
+                                                (18, 127, 16, "f32", 130, 127), (35, 4, 4, "f32", 8, 4)])
+def test_backward_of_few_experts_many_choices_and_strides(T, E, k, dtype, ldl, ldd):
+    z = draw(T, E, dtype, T, width=ldl)
+    ids, _ = run(z, T, E, k, R.SIGMOID, None, False, 1.0, ldl=ldl)
+    dw = np.random.default_rng(T).standard_normal((T, k)).astype(np.float32)
+    zf = z.float().cpu().numpy()[:, :E]
+    for score in (R.SOFTMAX, R.SIGMOID):
+        for renorm in (False, True):
+            dz = torch.full((T, ldd), 9.0, dtype=z.dtype, device="cuda")
+            m.moe_router_topk_backward(z, m.MOE_BF16 if dtype == "bf16" else m.MOE_F32, ldl, ids, dev_f32(dw), T, E, k, score, int(renorm), 1.5,
+                                       dz, ldd)
+            o, mag = R.router_topk_backward(zf, host(ids), dw, score, renorm, 1.5)
+            got = dz.float().cpu().numpy().astype(np.float64)
+            D = np.maximum(span(zf, np.tile(np.arange(E), (T, 1))).max(-1), 0.0)[:, None]
+            lim = (4 * D + 160) * U * mag
+            assert (np.abs(got[:, :E] - o) <= lim + (2.0 ** -8 * (np.abs(o) + lim) if dtype == "bf16" else 0.0) + 1e-36).all(), (score, renorm)
+            assert (got[:, E:] == 9).all()
