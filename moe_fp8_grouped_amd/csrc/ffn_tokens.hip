@@ -13,10 +13,11 @@
 //   2  y[slot] of 32 output channels
 // and the third adds each token's slots in slot order.
 //
-// Weights once at 5.2 TB/s against measured, three launches and the routing
-// (about 8 us) included: one token of 7168, 8 experts of 2048 in e4m3 68 us,
-// 83; 16 tokens of 2048, 8 of 64 experts of 768 in 4 bits 27, 53; 64 such
-// tokens in e4m3 58, 78.
+// Memory bounds it, then three launches and, in each, the routing, the first
+// loads and the tail.  Weights once at 5.2 TB/s, measured, and the first two
+// kernels' rates: one token of 7168, 8 experts of 2048 in e4m3 68 us, 82, 5.2
+// and 4.3 TB/s; 16 tokens of 2048, 8 of 64 experts of 768 in 4 bits 27, 51, 3.7
+// and 2.3; 64 such tokens in e4m3 58, 77, 5.1 and 3.9.
 #include "mx4_common.hpp"
 #include "tile_common.hpp"
 

@@ -134,7 +134,7 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const void* __restrict
     } else {
       key = static_cast<uint64_t>(order_key(z[i])) << 32;
     }
-    hi[i] = e < E ? static_cast<uint32_t>(key >> 32) : 0;   // (0 is below every expert's)
+    hi[i] = e < E ? max(static_cast<uint32_t>(key >> 32), 1u) : 0;   // (0: no expert, or chosen; a NaN's key may be 0 too)
     lo[i] = static_cast<uint32_t>(key);
   }
   float my_z = -INFINITY;                    // lane j: the j-th choice

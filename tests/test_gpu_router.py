@@ -229,3 +229,18 @@ def test_backward_of_few_experts_many_choices_and_strides(T, E, k, dtype, ldl, l
             lim = (4 * D + 160) * U * mag
             assert (np.abs(got[:, :E] - o) <= lim + (2.0 ** -8 * (np.abs(o) + lim) if dtype == "bf16" else 0.0) + 1e-36).all(), (score, renorm)
             assert (got[:, E:] == 9).all()
+
+
+def test_ids_stay_valid_without_finite_keys():
+    """Outside what is supported: a bias that is not finite, logits of +inf.  The choice is unspecified, its ids are not."""
+    E, k, T = 70, 8, 6
+    z = draw(T, E, "f32", 1)
+    z[1, ::3] = float("inf")
+    bits = np.full(E, 0xFFFFFFFF, np.uint32)
+    bits[1::4] = 0x7FC00000
+    bits[2::4] = 0xFF800000
+    for bias in (None, dev_f32(bits.view(np.float32))):
+        for score in (R.SOFTMAX, R.SIGMOID):
+            ids, _ = run(z, T, E, k, score, bias, True, 1.0)
+            for row in host(ids):
+                assert len(set(row.tolist())) == k and (row >= 0).all() and (row < E).all()
