@@ -185,7 +185,8 @@ def _ptr_rows(t, ld):
         return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("tensor arguments must be torch tensors in GPU memory")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) != ld):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1) or (shape[0] > 1 and stride[0] != ld):
         raise ValueError("expected a 2-D view with rows %d elements apart" % ld)
     return t.data_ptr()
 

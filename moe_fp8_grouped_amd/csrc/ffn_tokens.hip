@@ -15,9 +15,9 @@
 //
 // Memory bounds it, then three launches and, in each, the routing, the first
 // loads and the tail.  Weights once at 5.2 TB/s, measured, and the first two
-// kernels' rates: one token of 7168, 8 experts of 2048 in e4m3 68 us, 82, 5.2
-// and 4.3 TB/s; 16 tokens of 2048, 8 of 64 experts of 768 in 4 bits 27, 51, 3.7
-// and 2.3; 64 such tokens in e4m3 58, 77, 5.1 and 3.9.
+// kernels' rates: one token of 7168, 8 experts of 2048 in e4m3 68 us, 76, 5.5
+// and 4.1 TB/s; 16 tokens of 2048, 8 of 64 experts of 768 in 4 bits 27, 51, 3.8
+// and 2.3; 64 such tokens in e4m3 58, 70, 5.5 and 4.0.
 #include "mx4_common.hpp"
 #include "tile_common.hpp"
 
@@ -255,6 +255,18 @@ struct Loader {
       begin();
     }
   }
+  // AUX 2: not kept in the caches.  Weights that one pass reads are read once (one token e4m3 83 -> 75 us, 64 tokens
+  // 77 -> 69); those of an expert with more slots than a pass takes are read again.
+  __device__ __forceinline__ void load() {
+    if (seg.passes == 1)
+      load<2>();
+    else
+      load<0>();
+    ++q;
+    c += step;
+    settle();
+  }
+  template <int AUX>
   __device__ __forceinline__ void load() {
     const int slot = q % kRing, rowb = static_cast<int>(m.K / (MX4 ? 2 : 1));
     uint8_t* wd = sm.w[wave][slot];
@@ -265,7 +277,7 @@ struct Loader {
     for (int i = 0; i < 4; ++i) {
       const int b = min(128 * c + 16 * (sp ^ (i & 1)), rowb - 16);
       __builtin_amdgcn_global_load_lds((i < 2 ? w0 : w1) + static_cast<uint32_t>((8 * (i & 1) + row) * rowb + b),
-                                       (lds_void*)(wd + 1024 * i), 16, 0, 0);
+                                       (lds_void*)(wd + 1024 * i), 16, 0, AUX);
     }
     if constexpr (MX4) {                           // the three dwords that hold a row's eight scales
       const int kb = static_cast<int>(m.K / 32);
@@ -280,9 +292,6 @@ struct Loader {
       const int ch = m.nb == m.N ? lane & 15 : 0;
       if (lane < 32) __builtin_amdgcn_global_load_lds((lane < 16 ? s0 : s1) + 4 * (block + ch), (lds_void*)sd, 4, 0, 0);
     }
-    ++q;
-    c += step;
-    settle();
   }
 };
 

@@ -22,7 +22,10 @@
 //     rows of 2048 by 64 groups of 1536 columns 132 us, 1.55 PFLOP/s (as
 //     256 x 256 tiles with the weights through LDS: 142).
 //   fewer tiles than workgroups: 64-column tiles (run_tile, one column
-//     fragment a wave).
+//     fragment a wave): 512 ragged rows of 2080 by 1040 columns 18 us, with
+//     256-column tiles 30; the two above would take 352 and 200.
+// Weights kept out of the caches (they are read by two row tiles) cost the
+// first case 27 us.
 #include <type_traits>
 
 #include "mx4_common.hpp"

@@ -9,6 +9,15 @@ namespace moe {
 namespace {
 using namespace mx4;
 
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+// Read once here, and not kept in the caches: 8 experts of 7168 by 2048 to
+// codes and back 114 us instead of 131, 8192 rows of 7168 54 instead of 60.
+__device__ __forceinline__ uint4 load_once(const uint16_t* p) {
+  return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p)));
+}
+
 // Eight values to codes: v / 2^(s - 127), to the nearest even, saturating; a
 // block that is not finite has codes 0.
 __device__ __forceinline__ uint32_t encode8(const float (&v)[8], uint32_t s) {
@@ -25,7 +34,7 @@ __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(
 
 // Four lanes hold one block, eight elements each; a wave takes 64 such chunks
 // of kRowsAWave rows, its loads first.  Memory bounds it: 8192 rows of 7168 to
-// codes and back 60 us, 4.4 TB/s (a flat loop with a division a chunk and the
+// codes and back 52 us, 5.1 TB/s (a flat loop with a division a chunk and the
 // codes from comparisons: 93).
 constexpr int kRowsAWave = 4;
 
@@ -42,8 +51,8 @@ __global__ __launch_bounds__(256) void quantize_rows_mx4_kernel(const uint16_t* 
 #pragma unroll
     for (int u = 0; u < kRowsAWave; ++u) {
       const int64_t r = min(r0 + u * step, R - 1);
-      a[u] = *reinterpret_cast<const uint4*>(x + r * ldx + 8 * c);
-      if constexpr (SILU) b[u] = *reinterpret_cast<const uint4*>(x_up + r * ldx + 8 * c);
+      a[u] = load_once(x + r * ldx + 8 * c);
+      if constexpr (SILU) b[u] = load_once(x_up + r * ldx + 8 * c);
     }
 #pragma unroll
     for (int u = 0; u < kRowsAWave; ++u) {
@@ -76,7 +85,7 @@ __global__ __launch_bounds__(256) void quantize_rows_mx4_kernel(const uint16_t* 
 // elements of two neighbouring channels (a wave 256 bytes of a row of w), and
 // the codes go through LDS, so that a channel's eight blocks leave as one
 // 128-byte line.  Memory bounds it: 8 experts of 7168 by 2048 to codes and
-// back 131 us, 4.1 TB/s (a thread a block, its 16 bytes written where they are
+// back 104 us, 5.1 TB/s (a thread a block, its 16 bytes written where they are
 // formed, 64 channels apart: 177).
 constexpr int kTileN = 128, kTileB = 8, kTilePitch = kTileB * 16 + 16;
 
@@ -95,7 +104,7 @@ __global__ __launch_bounds__(256) void quantize_weights_mx4_kernel(const uint16_
         const uint16_t* p = w + (e * K + (b0 + j) * kBlock) * N + n;
         uint32_t pair[kBlock];
 #pragma unroll
-        for (int u = 0; u < kBlock; ++u) pair[u] = *reinterpret_cast<const uint32_t*>(p + u * N);
+        for (int u = 0; u < kBlock; ++u) pair[u] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p + u * N));
         uint32_t top[2] = {0, 0}, o[2][4];
 #pragma unroll
         for (int u = 0; u < kBlock; ++u) {   // bfloat16 magnitudes order as their bits do
@@ -129,8 +138,12 @@ __global__ __launch_bounds__(256) void quantize_weights_mx4_kernel(const uint16_
     }
 }
 
-// As quantize_rows: eight elements a lane, several rows a wave.
-template <bool BF16>
+// As quantize_rows: eight elements a lane, several rows a wave.  STREAM: a
+// result larger than the L2s together (32 MiB) leaves past them: there and back
+// as above 104 us instead of 114.
+constexpr int64_t kStreamBytes = 32 << 20;
+
+template <bool BF16, bool STREAM>
 __global__ __launch_bounds__(256) void dequantize_rows_mx4_kernel(const uint8_t* __restrict__ q, int64_t ldq,
                                                                   const uint8_t* __restrict__ scale, int64_t lds,
                                                                   int64_t R, int64_t C, void* __restrict__ out,
@@ -158,14 +171,25 @@ __global__ __launch_bounds__(256) void dequantize_rows_mx4_kernel(const uint8_t*
         o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[u], sv, 2));
         o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[u], sv, 3));
         if (s[u] == 255u) o[0] = o[1] = o[2] = o[3] = 0x7fc07fc0u;
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + r * ldo + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+        v4u* p = reinterpret_cast<v4u*>(static_cast<uint16_t*>(out) + r * ldo + 8 * c);
+        const v4u v = {o[0], o[1], o[2], o[3]};
+        if (STREAM)
+          __builtin_nontemporal_store(v, p);
+        else
+          *p = v;
       } else {
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = decode((w[u] >> (4 * i)) & 15u) * sv;
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + r * ldo + 8 * c);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        v4f* p = reinterpret_cast<v4f*>(static_cast<float*>(out) + r * ldo + 8 * c);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const v4f f = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+          if (STREAM)
+            __builtin_nontemporal_store(f, p + h);
+          else
+            p[h] = f;
+        }
       }
     }
   }
@@ -226,10 +250,14 @@ extern "C" int moe_dequantize_rows_mx4(const uint8_t* q, int64_t ldq, const uint
   if (!moe::aligned(q, 16) || !moe::aligned(out, 16)) return MOE_ERR_SHAPE;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const dim3 grid = moe::rows_grid(R, C);
-  if (out_dtype == MOE_BF16)
-    moe::dequantize_rows_mx4_kernel<true><<<grid, 256, 0, st>>>(q, ldq, scale, lds, R, C, out, ldo);
-  else
-    moe::dequantize_rows_mx4_kernel<false><<<grid, 256, 0, st>>>(q, ldq, scale, lds, R, C, out, ldo);
+  const bool bf = out_dtype == MOE_BF16, stream_out = R * C * (bf ? 2 : 4) > moe::kStreamBytes;
+#define MOE_DEQUANTIZE(B, S) moe::dequantize_rows_mx4_kernel<B, S><<<grid, 256, 0, st>>>(q, ldq, scale, lds, R, C, out, ldo)
+  if (bf) {
+    if (stream_out) MOE_DEQUANTIZE(true, true); else MOE_DEQUANTIZE(true, false);
+  } else {
+    if (stream_out) MOE_DEQUANTIZE(false, true); else MOE_DEQUANTIZE(false, false);
+  }
+#undef MOE_DEQUANTIZE
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }
