@@ -311,3 +311,16 @@ def test_gmm_enough_tiles_for_the_wide_kernel(K, N, fmt):
         assert err == 0
         (check_f32 if dtype == m.MOE_F32 else check_bf16)(g, o, A, "wide", hw_allowance=B if fmt == m.MOE_E4M3FN else None)
         assert (g[n:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,R", [(m.MOE_BF16, 2501), (m.MOE_F32, 1251)])
+def test_read_back_more_than_the_caches_hold(dtype, R):
+    """Results larger than the L2s leave past them: the same values, and rows of a wider buffer keep what lies beside."""
+    C, ld = 7168, 7176
+    rng = np.random.default_rng(R)
+    q = rng.integers(0, 256, (R, C // 2), dtype=np.uint8)
+    s = rng.integers(100, 150, (R, C // 32), dtype=np.uint8)
+    out = torch.full((R, ld), 9.0, dtype=torch.float32 if dtype == m.MOE_F32 else torch.bfloat16, device="cuda")
+    m.moe_dequantize_rows_mx4(dev_u8(q), C // 2, dev_u8(s), C // 32, R, C, dtype, out[:, :C], ld)
+    got = out.float().cpu().numpy()
+    assert np.array_equal(got[:, :C], mx4.decode(q, s).astype(np.float32)) and (got[:, C:] == 9).all()
