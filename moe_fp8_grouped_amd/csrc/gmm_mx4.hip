@@ -22,7 +22,7 @@
 //     rows of 2048 by 64 groups of 1536 columns 132 us, 1.55 PFLOP/s (as
 //     256 x 256 tiles with the weights through LDS: 142).
 //   fewer tiles than workgroups: 64-column tiles (run_tile, one column
-//     fragment a wave): 512 ragged rows of 2080 by 1040 columns 18 us, with
+//     fragment a wave): 512 ragged rows of 2080 by 1040 columns 15 us, with
 //     256-column tiles 30; the two above would take 352 and 200.
 // Weights kept out of the caches (they are read by two row tiles) cost the
 // first case 27 us.
@@ -62,6 +62,7 @@ struct Mx4Args {
   int64_t M, K, N;
   void* out;
   int32_t* err;
+  int tile_rows;               // rows a tile holds at most
 };
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -668,7 +669,6 @@ __global__ __launch_bounds__(CF == 4 && !A8 ? kWideThreads : kThreads, 2) void g
   using LDS = std::conditional_t<WIDE, WideLds, Lds<A8>>;
   __shared__ __attribute__((aligned(1024))) LDS sm;
   constexpr int BN = 64 * CF, THREADS = WIDE ? kWideThreads : kThreads;
-  constexpr int ROWS = WIDE ? kWideRows : kRows;
   const int NT = static_cast<int>((p.N + BN - 1) / BN);
   // the group table lives in the stages while tiles are decoded, up to kDesc at a time
   struct Table {
@@ -693,7 +693,7 @@ __global__ __launch_bounds__(CF == 4 && !A8 ? kWideThreads : kThreads, 2) void g
     const bool over = wave0_scan_sat(gt.tmp, gt.rows_off, p.El, p.M);
     if (over && tid == 0 && blockIdx.x == 0) raise_error(p.err, MOE_DEVERR_ROWS);
     __syncthreads();
-    for (int g = tid; g < p.El; g += THREADS) gt.tmp[g] = row_tiles(gt.rows_off[g + 1] - gt.rows_off[g], ROWS) * NT;
+    for (int g = tid; g < p.El; g += THREADS) gt.tmp[g] = row_tiles(gt.rows_off[g + 1] - gt.rows_off[g], p.tile_rows) * NT;
     __syncthreads();
     wave0_scan(gt.tmp, gt.tiles_off, p.El);
     __syncthreads();
@@ -703,7 +703,7 @@ __global__ __launch_bounds__(CF == 4 && !A8 ? kWideThreads : kThreads, 2) void g
     if (tid < min(left, kDesc)) {
       const int t = first + (base + tid) * step;
       const int g = find_group(gt, p.El, t);
-      const int m = gt.rows_off[g + 1] - gt.rows_off[g], nb = row_tiles(m, ROWS), fr = tile_frags(m, nb);
+      const int m = gt.rows_off[g + 1] - gt.rows_off[g], nb = row_tiles(m, p.tile_rows), fr = tile_frags(m, nb);
       const int local = t - gt.tiles_off[g], ct = local / nb, rt = local - ct * nb;
       // (even filling may leave a last tile without rows)
       sm.desc[tid] = make_int4(gt.rows_off[g] + 16 * fr * rt, ct, g, min(16 * fr, m - 16 * fr * rt));
@@ -766,13 +766,18 @@ __global__ __launch_bounds__(256) void align_scales_kernel(const uint8_t* __rest
 }
 
 template <bool A8, bool OUT_BF16>
-hipError_t launch(const Mx4Args& p, hipStream_t st) {
+hipError_t launch(Mx4Args p, hipStream_t st) {
   // 256-column tiles when they fill the GPU's workgroups (4-bit rows: one a CU, e4m3: two), 64-column ones otherwise
   const int64_t groups = p.El < p.M ? p.El : p.M;
   const int64_t wide_rows = A8 ? kRows : kWideRows, wide_slots = (A8 ? 2 : 1) * num_cus();
   const bool wide = (groups + p.M / wide_rows) * moe_cdiv(p.N, 256) >= wide_slots;
-  const int64_t most = (moe_cdiv(p.M, wide ? wide_rows : kRows) + groups) * moe_cdiv(p.N, wide ? 256 : 64);
   const int64_t slots = wide ? wide_slots : 2 * num_cus();
+  const int64_t col_tiles = moe_cdiv(p.N, wide ? 256 : 64);
+  // 64-column tiles: of half the rows as long as every one has a workgroup (512 ragged rows by 1040 columns: 15.1 us
+  // with 64 rows, 18.2 with 128, 20.2 with 32)
+  const bool half = !wide && (moe_cdiv(p.M, kRows / 2) + groups) * col_tiles <= slots;
+  p.tile_rows = static_cast<int>(wide ? wide_rows : half ? kRows / 2 : kRows);
+  const int64_t most = (moe_cdiv(p.M, p.tile_rows) + groups) * col_tiles;
   const unsigned grid = static_cast<unsigned>(most < 8 ? 8 : most < slots ? most : slots);   // each XCD's part has its own workgroups
   if (wide)
     gmm_mx4_kernel<A8, OUT_BF16, 4><<<grid, A8 ? kThreads : kWideThreads, 0, st>>>(p);
@@ -820,7 +825,7 @@ extern "C" int moe_gmm_mx4(const uint8_t* lhs, int64_t ldl, const void* lhs_scal
   if (!ws || ws_bytes < moe::gmm_mx4_ws_bytes(M, K)) return MOE_ERR_WORKSPACE;
   hipStream_t st = static_cast<hipStream_t>(stream);
   moe::Mx4Args p{lhs, ldl, lhs_scale, lds, lhs_scale_mode == MOE_SCALE_ROW_DYNAMIC ? 1 : 0, rhs, rhs_scale,
-                 group_sizes, group_offset, num_local_experts, M, K, N, out, static_cast<int32_t*>(ws)};
+                 group_sizes, group_offset, num_local_experts, M, K, N, out, static_cast<int32_t*>(ws), 0};
   if (!a8 && num_local_experts > 0 && (lds % 4 || reinterpret_cast<uintptr_t>(lhs_scale) % 4)) {
     const int kb = static_cast<int>(K / 32);
     uint8_t* rows = static_cast<uint8_t*>(ws) + moe::tile::kHdr;
