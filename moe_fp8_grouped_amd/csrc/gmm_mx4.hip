@@ -423,8 +423,10 @@ __device__ __forceinline__ void run_tile(const Mx4Args& p, Lds<A8>& sm, const Ti
     const int win = (q / 4) & 1;
     uint32_t ws[CF];
     read_scales<CF>(wsa0 + 4 * (q % 4) + win * static_cast<int>(sizeof(sm.ws[0])), ws);
-    if (END && q >= NP - 1) {                    // blocks past K: zero weights with a plain scale
-      const bool past = 4 * q + grp >= kb;
+    // blocks past K: zero weights, and plain scales for both operands (a 4-bit row's byte there is not its own: it lies
+    // between the rows or is the next row's, and a NaN would turn the zeros into NaN)
+    const bool past = END && 4 * q + grp >= kb;
+    if (END && q >= NP - 1) {
 #pragma unroll
       for (int f = 0; f < CF; ++f) {
         wf(f).x = past ? 0 : wf(f).x;
@@ -455,6 +457,7 @@ __device__ __forceinline__ void run_tile(const Mx4Args& p, Lds<A8>& sm, const Ti
         read_rows4<N>(xa + 2048 * i0, xsa + 16 * kPitch * i0, x, xs);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
+          if (END) xs[j] = past ? 127 : xs[j];
           const v8i xv = {x[j][0], x[j][1], x[j][2], x[j][3], 0, 0, 0, 0};
 #pragma unroll
           for (int f = 0; f < CF; ++f) acc[i0 + j][f] = mfma_mx4<false>(frag16(wf(f)), ws[f], xv, xs[j], acc[i0 + j][f]);
@@ -621,8 +624,8 @@ __device__ __forceinline__ void run_wide(const Mx4Args& p, WideLds& sm, const Ti
       w[f] = __builtin_bit_cast(uint4, lds_read<v4i>(wb + f * 4 * B));
       ws[f] = lds_read<uint8_t>(wsa0 + win * static_cast<uint32_t>(sizeof(sm.ws[0])) + sc + f * 4 * kPitch);
     }
-    if (END && s == NS - 1) {                    // blocks past K: zero weights with a plain scale
-      const bool past = 4 * s + grp >= kb;
+    const bool past = END && 4 * s + grp >= kb;  // blocks past K: zero weights, plain scales for both operands
+    if (END && s == NS - 1) {
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
         w[f].x = past ? 0 : w[f].x;
@@ -636,7 +639,8 @@ __device__ __forceinline__ void run_wide(const Mx4Args& p, WideLds& sm, const Ti
     for (int i = 0; i < MI; ++i) {
       const v4i v = lds_read<v4i>(xb + 16 * B * i);
       const v8i x{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
-      const uint32_t xs = lds_read<uint8_t>(xsa0 + win * static_cast<uint32_t>(sizeof(sm.xs[0])) + sc + 16 * kPitch * i);
+      uint32_t xs = lds_read<uint8_t>(xsa0 + win * static_cast<uint32_t>(sizeof(sm.xs[0])) + sc + 16 * kPitch * i);
+      if (END) xs = past ? 127 : xs;
 #pragma unroll
       for (int f = 0; f < 4; ++f) acc[i][f] = mfma_mx4<false>(frag16(w[f]), ws[f], x, xs, acc[i][f]);
     }

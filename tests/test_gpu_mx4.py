@@ -324,3 +324,67 @@ def test_read_back_more_than_the_caches_hold(dtype, R):
     m.moe_dequantize_rows_mx4(dev_u8(q), C // 2, dev_u8(s), C // 32, R, C, dtype, out[:, :C], ld)
     got = out.float().cpu().numpy()
     assert np.array_equal(got[:, :C], mx4.decode(q, s).astype(np.float32)) and (got[:, C:] == 9).all()
+
+
+# ------------------------------------------ what lies beside a row's scales
+def drawn_problem(rng, K, N, El):
+    """(El = 32 at 2064 columns: enough tiles for the 256-column kernel; otherwise the 64-column one.)"""
+    gs = rng.integers(0, 9, El).astype(np.int32)
+    gs[:3] = [5, 1, 17]
+    M = int(gs.sum())
+    q = rng.integers(0, 256, (El, N, K // 2), dtype=np.uint8)
+    s = rng.integers(120, 128, (El, N, K // 32), dtype=np.uint8)
+    lq = rng.integers(0, 256, (M, K // 2), dtype=np.uint8)
+    ls = rng.integers(120, 128, (M, K // 32), dtype=np.uint8)
+    return gs, M, dev_u8(q), dev_u8(s), lq, ls
+
+
+def padded(ls, lds, fill):
+    wide = np.full((ls.shape[0], lds), fill, np.uint8)
+    wide[:, :ls.shape[1]] = ls
+    return dev_u8(wide)[:, :ls.shape[1]]
+
+
+@pytest.mark.parametrize("N,El", [(80, 3), (2064, 32)])
+@pytest.mark.parametrize("K", [32, 128, 160, 384, 608, 1312])
+def test_gmm_bytes_between_the_rows_scales_take_no_part(K, N, El):
+    """NaN's code in the padding that the format's quantizer leaves as it is: the same bits as with a plain scale there."""
+    rng = np.random.default_rng([K, N])
+    gs, M, q, s, lq, ls = drawn_problem(rng, K, N, El)
+    kb = K // 32
+    for lds in (-(-kb // 4) * 4 + 4, kb + 3):                # read in place where dword aligned, else copied first
+        got = [run_gmm(dev_u8(lq), padded(ls, lds, fill), m.MOE_MX4, m.MOE_SCALE_ROW_DYNAMIC, q, s, gs, El, 0, El, M, K, N, m.MOE_F32, lds=lds)[0]
+               for fill in (127, 255)]
+        assert np.isfinite(got[0]).all() and np.array_equal(got[0], got[1]), lds
+
+
+@pytest.mark.parametrize("N,El", [(80, 3), (2064, 32)])
+@pytest.mark.parametrize("K", [128, 160, 384, 640, 2080, 2176])
+def test_gmm_a_row_without_values_leaves_its_neighbours(K, N, El):
+    """Compact scale rows: NaN scales in row 3 and in the first row of the second group."""
+    rng = np.random.default_rng([K, N, 1])
+    gs, M, q, s, lq, ls = drawn_problem(rng, K, N, El)
+    clean, _ = run_gmm(dev_u8(lq), dev_u8(ls), m.MOE_MX4, m.MOE_SCALE_ROW_DYNAMIC, q, s, gs, El, 0, El, M, K, N, m.MOE_F32)
+    bad = [3, 5]
+    ls[bad] = 255
+    got, _ = run_gmm(dev_u8(lq), dev_u8(ls), m.MOE_MX4, m.MOE_SCALE_ROW_DYNAMIC, q, s, gs, El, 0, El, M, K, N, m.MOE_F32)
+    keep = np.ones(M, bool)
+    keep[bad] = False
+    assert np.isnan(got[bad]).all() and np.isfinite(clean).all()
+    assert np.array_equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("N,El", [(80, 3), (2064, 32)])
+def test_gmm_scale_rows_copied_into_a_used_workspace(N, El):
+    K, kb = 160, 5                                           # five bytes a row: copied to eight
+    rng = np.random.default_rng(N)
+    gs, M, q, s, lq, ls = drawn_problem(rng, K, N, El)
+    got = []
+    for fill in (0, 255):
+        ws = m.workspace(m.MOE_OP_GMM_MX4, M, K, N, El)
+        ws[256:] = fill
+        out = torch.empty(M, N, device="cuda")
+        m.moe_gmm_mx4(dev_u8(lq), K // 2, dev_u8(ls), kb, m.MOE_MX4, m.MOE_SCALE_ROW_DYNAMIC, q, s, dev_i32(gs), El, 0, El, M, K, N, m.MOE_F32,
+                      out, ws)
+        got.append(host(out))
+    assert np.isfinite(got[0]).all() and np.array_equal(got[0], got[1])
