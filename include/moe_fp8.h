@@ -673,7 +673,8 @@ int moe_gmm_mx4(const uint8_t* lhs, int64_t ldl, const void* lhs_scale, int64_t 
  * for many tokens; here the rows are not sorted and nothing is quantized: the
  * activations stay bfloat16, sums and the hidden values 32-bit (the hidden
  * values enter the second product as two bfloat16 pieces), one rounding at
- * the end.  A token's result does not depend on the other tokens' values.
+ * the end.  A token's result does not depend on the other tokens, neither on
+ * their values nor on their experts: the same bits alone and in any batch.
  *   x        [T, H] bf16, rows ldx elements apart (a multiple of 8, 16-byte
  *            aligned); 0 <= T <= 64, T k <= 1024 (MOE_ERR_UNSUPPORTED beyond).
  *   expert_ids, topk_weights [T, k] int32 / f32, as moe_router_topk writes

@@ -5,7 +5,8 @@
 // converted on the way to the matrix cores, while the activations stay as
 // they are (bfloat16 rows; the hidden values as two bfloat16 pieces, 16 bits
 // of mantissa, since they are small next to the weights) -- nothing is
-// quantized, so a token's result does not depend on the others'.
+// quantized, and every sum's order is fixed, so a token's result does not
+// depend on the others'.
 //
 // The first two form weights (16 output channels) times rows (16 slots) with
 // v_mfma_f32_16x16x32_bf16, 32 channels a wave at a time (a unit):
@@ -164,7 +165,10 @@ __device__ __forceinline__ v4f mfma_bf16(const bf8& a, const bf8& b, const v4f& 
 // The units of one call, in a run over the met experts, and this workgroup's
 // part of them, in segments of one expert each.  A segment's units go to the
 // four waves in turn, each wave a unit of its own; the one to three left over
-// are formed by all four waves together, which split the contraction.
+// are formed by all four waves together, which split the contraction.  Which
+// of the two a unit falls to depends on the other tokens' experts, and a
+// token's result must not: either way chunk c of the contraction goes to sum
+// c % 4 of four, which are added as (0 + 1) + (2 + 3).
 struct Segment {
   int first, last, expert;                         // units; index of the met expert
   int full, jobs, passes;                          // units a wave of its own; jobs a pass; passes of 16 slots
@@ -205,6 +209,7 @@ struct Loader {
   Lds& sm;
   Segment seg;
   int end, units, chunks, wave, lane;
+  int block_len;                                   // e4m3: elements of a K block (32-bit: a 64-bit division is most of this code)
   int pass, job, c, step, q;                       // q: chunks loaded so far
   bool more;
   const uint8_t *w0, *w1, *s0, *s1;                // of the job
@@ -212,6 +217,7 @@ struct Loader {
   __device__ __forceinline__ Loader(const Weights<UP>& m, Lds& sm, int first, int end, int units, int wave, int lane)
       : m(m), sm(sm), end(end), units(units), wave(wave), lane(lane) {
     chunks = static_cast<int>((m.K / (MX4 ? 2 : 1) + 127) / 128);
+    if constexpr (!MX4) block_len = static_cast<int>(m.K) / m.kb;
     q = 0;
     more = first < end;
     if (more) {
@@ -235,8 +241,9 @@ struct Loader {
       s1 = static_cast<const uint8_t*>(m.s) + (e * m.N + r1) * (m.K / 32);
     } else {                                       // one K block's factors: a channel's own, or its column block's
       const float* s = static_cast<const float*>(m.s) + e * m.kb * m.nb;
-      s0 = reinterpret_cast<const uint8_t*>(s + r0 / (m.N / m.nb));
-      s1 = reinterpret_cast<const uint8_t*>(s + r1 / (m.N / m.nb));
+      const int wide = static_cast<int>(m.N) / m.nb;
+      s0 = reinterpret_cast<const uint8_t*>(s + static_cast<int>(r0) / wide);
+      s1 = reinterpret_cast<const uint8_t*>(s + static_cast<int>(r1) / wide);
     }
   }
   __device__ __forceinline__ void settle() {       // (a short row may leave a wave without a chunk of a split unit)
@@ -288,7 +295,7 @@ struct Loader {
         if (idx < 96) __builtin_amdgcn_global_load_lds((r < 16 ? s0 : s1) + b, (lds_void*)(sd + 256 * i), 4, 0, 0);
       }
     } else {
-      const int64_t block = m.kb > 1 ? (static_cast<int64_t>(128) * c / (m.K / m.kb)) * m.nb : 0;
+      const int64_t block = static_cast<int64_t>(128 * c / block_len) * m.nb;
       const int ch = m.nb == m.N ? lane & 15 : 0;
       if (lane < 32) __builtin_amdgcn_global_load_lds((lane < 16 ? s0 : s1) + 4 * (block + ch), (lds_void*)sd, 4, 0, 0);
     }
@@ -353,13 +360,14 @@ __device__ __forceinline__ void run_units(const Weights<UP>& m, Lds& sm, const F
       if (KC == K) stage(0);
       for (int job = 0; job < seg.jobs; ++job) {
         const bool own = job < seg.full;
-        v4f acc[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
+        v4f sums[kWaves][2];                       // (of a split unit each wave fills its first)
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) sums[w][0] = sums[w][1] = v4f{0.f, 0.f, 0.f, 0.f};
         int c = own ? 0 : wave;
         for (int k0 = 0; k0 < K; k0 += KC) {
           if (KC < K) stage(k0);
           const int stop = min((k0 + KC + CK - 1) / CK, chunks);
-#pragma clang loop unroll(disable)
-          for (; c < stop; c += own ? 1 : kWaves) {
+          auto chunk = [&](int c, v4f(&acc)[2]) __attribute__((always_inline)) {
             const int slot_at = q % kRing;
             if (load.more)                         // then all kRing - 1 later chunks are in flight, in order
               __builtin_amdgcn_s_waitcnt(waitcnt_vm((kRing - 1) * L::kLoads));
@@ -433,17 +441,34 @@ __device__ __forceinline__ void run_units(const Weights<UP>& m, Lds& sm, const F
                 for (int i = 0; i < 4; ++i) acc[r][i] = fmaf(sc[r][i], part[i], acc[r][i]);
               }
             }
+          };
+          // Four chunks a turn (one, where the unit is split; a part of the contraction ends at a multiple of four chunks,
+          // or at its end): the sums keep their registers.  Moved round by one a chunk, one copy of the code, the layer
+          // of 64 tokens took 86 us instead of 81.
+#pragma clang loop unroll(disable)
+          for (; c < stop; c += kWaves) {
+            if constexpr (MX4) {                   // in the accumulators' own registers (else moved there and back each turn: 56.5 us for 54.7)
+#pragma unroll
+              for (int w = 0; w < kWaves; ++w) asm volatile("" : "+a"(sums[w][0]), "+a"(sums[w][1]));
+            }
+            chunk(c, sums[0]);
+            if (!own) continue;
+            if (c + 1 < stop) chunk(c + 1, sums[1]);
+            if (c + 2 < stop) chunk(c + 2, sums[2]);
+            if (c + 3 < stop) chunk(c + 3, sums[3]);
           }
         }
         const int unit = unit_of(seg, job, wave) - seg.expert * units;
         if (own) {
-          finish(unit, slot, l15 < n, acc, 0, 4);
+          const v4f sum[2] = {(sums[0][0] + sums[1][0]) + (sums[2][0] + sums[3][0]),
+                              (sums[0][1] + sums[1][1]) + (sums[2][1] + sums[3][1])};
+          finish(unit, slot, l15 < n, sum, 0, 4);
         } else {                                   // wave w finishes element w of both blocks
           lds_barrier();
 #pragma unroll
           for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) lds_write<float>(lds_addr(&sm.red[wave][4 * r + i][lane]), acc[r][i]);
+            for (int i = 0; i < 4; ++i) lds_write<float>(lds_addr(&sm.red[wave][4 * r + i][lane]), sums[0][r][i]);
           lds_barrier();
           v4f sum[2];
 #pragma unroll

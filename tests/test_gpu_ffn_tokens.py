@@ -215,3 +215,38 @@ LONG = [  # rows and weights beyond what a workgroup stages or takes at once
 @pytest.mark.parametrize("case", LONG, ids=str)
 def test_long_rows_and_many_units(case):
     test_matches_the_oracle(case)
+
+
+@pytest.mark.parametrize("fmt", [m.MOE_MX4, m.MOE_E4M3FN])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_token_alone_and_in_a_batch_of_many_units(fmt, dtype):
+    """The batch gives every workgroup more than four units of an expert, the token alone one or two: units that a wave
+    forms by itself and units that four waves share."""
+    E, H, I, T = 16, 2560, 1600, 64
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    q, s, blocks = [], [], []
+    for N, K in ((2 * I, H), (H, I)):
+        if fmt == m.MOE_MX4:
+            q.append(torch.randint(0, 256, (E, N, K // 2), generator=gen, dtype=torch.uint8, device="cuda"))
+            s.append(torch.randint(118, 122, (E, N, K // 32), generator=gen, dtype=torch.uint8, device="cuda"))
+            blocks += [0, 0]
+        else:
+            q.append((torch.randn(E, N, K, generator=gen, device="cuda") * 0.5).to(torch.float8_e4m3fn).view(torch.uint8))
+            s.append(torch.rand(E, 1, 1, N, generator=gen, device="cuda") * 0.1)
+            blocks += [1, N]
+    x = torch.randn(T, H, generator=gen, device="cuda").to(torch.bfloat16)
+    ws = m.workspace(m.MOE_OP_FFN_TOKENS, T * 2, H, I, E)
+    for k in (1, 2):
+        ids = torch.rand(T, E, generator=gen, device="cuda").argsort(1)[:, :k].to(torch.int32).contiguous()
+        tw = torch.rand(T, k, generator=gen, device="cuda")
+
+        def call(rows):
+            n = len(rows)
+            out = torch.empty(n, H, dtype=dtype, device="cuda")
+            m.moe_ffn_tokens(x[rows].contiguous(), H, ids[rows].contiguous(), tw[rows].contiguous(), n, k, H, I, E, 0, E, fmt, q[0], s[0],
+                             blocks[0], blocks[1], q[1], s[1], blocks[2], blocks[3], m.MOE_F32 if dtype == torch.float32 else m.MOE_BF16, out, ws)
+            return out
+        batch = call(list(range(T)))
+        assert torch.isfinite(batch).all()
+        for rows in ([0], [31], [63], [5, 9], list(range(20, 33))):
+            assert torch.equal(call(rows), batch[rows]), (k, rows)
