@@ -687,7 +687,10 @@ int moe_gmm_mx4(const uint8_t* lhs, int64_t ldl, const void* lhs_scale, int64_t 
  *            nbo] under moe_gmm_fp8's rules; H and I multiples of 16.
  *            MOE_MX4: w01 [E_loc, 2I, H/2], wo [E_loc, H, I/2] codes, e8m0
  *            scales [E_loc, 2I, H/32] and [E_loc, H, I/32]; kb01 = nb01 = kbo
- *            = nbo = 0; H and I multiples of 32.
+ *            = nbo = 0; H and I multiples of 32.  A scale of 255 (NaN)
+ *            makes every result that its block enters NaN, whatever the codes.
+ *            Scales of 253 and 254 are not supported (their values may pass
+ *            bfloat16's range and become infinite; no quantizer here writes them).
  *   out      [T, H] bf16 (default) or f32.
  *   ws       workspace of moe_workspace_bytes(MOE_OP_FFN_TOKENS, T*k, H, I, E),
  *            zeroed once before its first use (the error word).  Calls that

@@ -250,3 +250,53 @@ def test_a_token_alone_and_in_a_batch_of_many_units(fmt, dtype):
         assert torch.isfinite(batch).all()
         for rows in ([0], [31], [63], [5, 9], list(range(20, 33))):
             assert torch.equal(call(rows), batch[rows]), (k, rows)
+
+
+@pytest.mark.parametrize("T", [1, 21])
+def test_weights_without_a_value_reach_their_own_results_only(T):
+    """Scale 255 (what the quantizer writes, with codes 0, for a block that is not finite) in one block."""
+    E, k, H, I = 4, 2, 288, 160
+    L = Layer(m.MOE_MX4, E, H, I, seed=T)
+    rng = np.random.default_rng([T, 5])
+    ids, tw = routing(rng, T, k, E)
+    ids[0] = [2, 1]
+    xb = to_bf16_bits(rng.standard_normal((T, H)).astype(np.float32))
+    xb[:, 64:96] = 0                                     # zeros at the block too: zero times NaN is NaN
+    out, ws = torch.empty(T, H, device="cuda"), L.ws(T, k, E)
+
+    def call():
+        L.call(dev_bf16(xb), H, dev_i32(ids), dev_f32(tw), T, k, E, 0, m.MOE_F32, out, ws)
+        return host(out).copy()
+    clean = call()
+    meets = (ids == 2).any(1)
+    for row in (17, I + 17):                             # a gate row, an up row: the whole token
+        q, s = L.q[0].clone(), L.s[0].clone()
+        L.q[0][2, row, 32:48], L.s[0][2, row, 2] = 0, 255
+        got = call()
+        assert np.isnan(got[meets]).all() and np.array_equal(got[~meets], clean[~meets])
+        L.q[0].copy_(q), L.s[0].copy_(s)
+    L.q[1][2, 100, 64:80], L.s[1][2, 100, 4] = 0, 255    # an output channel
+    got = call()
+    bad = np.zeros((T, H), bool)
+    bad[meets, 100] = True
+    assert np.isnan(got[bad]).all() and np.array_equal(got[~bad], clean[~bad])
+
+
+def test_smallest_and_largest_scales():
+    """Scale codes 0 (2^-127, below the normal range) and 252, the largest that a quantizer writes."""
+    T, k, E, H, I = 3, 1, 1, 64, 32
+    L = Layer(m.MOE_MX4, E, H, I, seed=3)
+    rng = np.random.default_rng(4)
+    ids = np.zeros((T, k), np.int32)
+    for up, down, xs, w in ((0, 127, 2.0 ** 122, 1.0), (252, 127, 2.0 ** -124, 1.0), (127, 0, 2.0 ** -4, 2.0 ** 120), (127, 252, 2.0 ** -10, 2.0 ** -120)):
+        q = [rng.integers(0, 256, tuple(v.shape), dtype=np.uint8) for v in L.q]
+        s = [np.full(tuple(v.shape), c, np.uint8) for v, c in zip(L.s, (up, down))]
+        L.q, L.s = [dev_u8(v) for v in q], [dev_u8(v) for v in s]
+        xb = to_bf16_bits((rng.standard_normal((T, H)) * xs).astype(np.float32))
+        tw = np.full((T, k), w, np.float32)
+        o, tol = ffn_tokens(xb, ids, tw, mx4.decode(q[0], s[0]), mx4.decode(q[1], s[1]), 0, E, E)
+        out, ws = torch.empty(T, H, device="cuda"), L.ws(T, k, E)
+        L.call(dev_bf16(xb), H, dev_i32(ids), dev_f32(tw), T, k, E, 0, m.MOE_F32, out, ws)
+        assert np.abs(o).max() > 1e-6
+        # a slot's own result near 2^-127 is held to 2^-149, the step of float32 there
+        check(host(out), o, tol + w * 2.0 ** -148, 2.0 ** -24)
