@@ -577,7 +577,8 @@ int moe_router_topk(const void* logits, int logits_dtype, int64_t ldl, int64_t T
  *   sigmoid, renormalize   the same with (g_e - sum_j g_j p_j / S) / S in
  *                          place of g_e, S = the chosen p's sum
  * Experts taken out by -inf, and every expert of a row without another
- * logit, get 0.
+ * logit, get 0, and dweights of slots that hold such an expert take no part,
+ * whatever they hold.
  *   logits .. weight_scale as in the forward call; expert_ids [T, k] as it
  *   wrote them (an id outside [0, E) takes no part; one given twice counts
  *   twice).

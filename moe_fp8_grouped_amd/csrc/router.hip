@@ -190,6 +190,8 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const void* __restrict
 //   sigmoid           dz_e = g_e p_e (1 - p_e)
 //   sigmoid, renorm.  the same with (g_e - sum_j g_j p_j / S) / S for g_e, S = sum of the chosen p
 // An index outside [0, E) takes no part; an index given twice counts twice.
+// An expert that was taken out has gradient 0 and its slots' gradients take
+// no part: a padded token's may hold anything.
 template <bool BF16, int V, bool SIGMOID>
 __global__ __launch_bounds__(256) void router_bwd_kernel(const void* __restrict__ logits, int64_t ldl,
                                                          const int32_t* __restrict__ ids,
@@ -216,6 +218,8 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(const void* __restrict_
     for (int i = 0; i < V; ++i)
       if (id == lane + 64 * i && id < E) { g[i] += dw; n[i] += 1.0f; }
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i) g[i] = z[i] == -INFINITY ? 0.0f : g[i];        // taken out: a gradient of any value counts nothing
   float m = -INFINITY;                       // over all experts, or the chosen ones
 #pragma unroll
   for (int i = 0; i < V; ++i) m = fmaxf(m, (!renorm || n[i] > 0.0f) ? z[i] : -INFINITY);
@@ -247,6 +251,7 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(const void* __restrict_
     } else {
       d = p[i] * inv * (g[i] - (renorm ? n[i] : 1.0f) * (dot * inv));
     }
+    if (z[i] == -INFINITY) d = 0.0f;
     if (BF16)
       static_cast<uint16_t*>(dlogits)[t * ldd + e] = f32_to_bf16(d);
     else
@@ -323,6 +328,10 @@ __global__ __launch_bounds__(256) void router_bwd_rows_kernel(const void* __rest
           if (d == 64 * i + c) { g[i][c] += dw; n[i][c] += 1.0f; }
     }
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) g[i][c] = z[i][c] == -INFINITY ? 0.0f : g[i][c];   // taken out: a gradient of any value counts nothing
   float m0 = -INFINITY;
   if (!SIGMOID) {                            // the maximum over all experts, or the chosen ones
 #pragma unroll
@@ -363,6 +372,7 @@ __global__ __launch_bounds__(256) void router_bwd_rows_kernel(const void* __rest
       } else {
         d[c] = p[i][c] * inv * (g[i][c] - (renorm ? n[i][c] : 1.0f) * (dot * inv));
       }
+      if (z[i][c] == -INFINITY) d[c] = 0.0f;
     }
     if (wide) {
       if (BF16)

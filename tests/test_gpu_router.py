@@ -244,3 +244,30 @@ def test_ids_stay_valid_without_finite_keys():
             ids, _ = run(z, T, E, k, score, bias, True, 1.0)
             for row in host(ids):
                 assert len(set(row.tolist())) == k and (row >= 0).all() and (row < E).all()
+
+
+# ------------------------------------- gradients of weights that were left out
+@pytest.mark.parametrize("E", [16, 96, 200])
+@pytest.mark.parametrize("score", [R.SOFTMAX, R.SIGMOID])
+@pytest.mark.parametrize("renorm", [0, 1])
+def test_gradients_of_masked_slots_take_no_part(E, score, renorm):
+    """A padded token's row, and slots whose expert was taken out: NaN and infinities there reach nothing."""
+    T, k = 21, 4
+    rng = np.random.default_rng([E, score, renorm])
+    z = rng.standard_normal((T, E)).astype(np.float32)
+    z[2::5] = -np.inf                                    # padded tokens
+    z[3::5, 2:] = -np.inf                                # two experts left for four slots
+    z[4, :] = np.nan
+    zd = torch.from_numpy(z).cuda()
+    ids, _ = run(zd, T, E, k, score, None, renorm, 1.0)
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    masked = ~np.isfinite(np.take_along_axis(z, host(ids).astype(np.int64), -1))
+    got = []
+    for fill in ((0.0,), (np.nan, np.inf, -np.inf)):
+        d = dw.copy()
+        d[masked] = np.resize(np.array(fill, np.float32), masked.sum())
+        dz = torch.full_like(zd, float("nan"))
+        m.moe_router_topk_backward(zd, m.MOE_F32, E, ids, dev_f32(d), T, E, k, score, renorm, 1.0, dz, E)
+        got.append(host(dz))
+    assert masked.sum() > 10 and np.isfinite(got[0]).all() and np.array_equal(got[0], got[1])
+    assert (got[1][~np.isfinite(z)] == 0).all()
