@@ -82,6 +82,30 @@ __device__ __forceinline__ uint32_t max_of(uint32_t v) {
   return over_wave(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
 
+// Sigmoids of renormalised weights where a chosen logit is below kLow: there
+// exp(-z) passes float32's range and p falls below its normal one, while the
+// ratios of the chosen p are ordinary numbers.  So p times one factor for the
+// row: with top, the largest chosen logit, below kLow too, p = exp(z) to
+// 2^-92 and the factor is exp(-top); otherwise it is 2^100.  The differences
+// z - top and z - kLow are exact wherever the result is not 0.  Below kNone p
+// is 0: a mask of the type's lowest value is no logit to compare with another.
+constexpr float kLow = -64.0f, kNone = -700.0f;
+__device__ __forceinline__ bool is_low(float z) { return z < kLow && z >= kNone; }
+__device__ __forceinline__ float sigmoid_times(float z, float top) {
+  if (z < kNone) return 0.0f;
+  if (top < kLow) return expf(z - top);
+  constexpr float kBig = 1267650600228229401496703205376.0f;          // 2^100
+  constexpr float kBigLow = 203.30718f;                               // 2^100 exp(kLow)
+  return z < kLow ? expf(z - kLow) * kBigLow : kBig / (1.0f + expf(-z));
+}
+
+// sigmoid(z), and 1 - sigmoid(z) without cancellation, from exp(-|z|), which stays in range
+__device__ __forceinline__ float sigmoid(float z, float& rest) {
+  const float e = expf(-fabsf(z)), near = 1.0f / (1.0f + e), far = e / (1.0f + e);
+  rest = z < 0.0f ? near : far;
+  return z < 0.0f ? far : near;
+}
+
 // One wave per row, expert e = lane + 64 i in register i.  Every choice is one
 // maximum over the wave (two for the bias's 64-bit keys), and ballots that find
 // its first expert.  8192 rows of 256 bf16 logits, k = 8: 10.2 us (with every
@@ -166,7 +190,9 @@ __global__ __launch_bounds__(256) void router_topk_kernel(const void* __restrict
   }
   float w;
   if (SIGMOID) {
-    w = 1.0f / (1.0f + expf(-my_z));
+    float rest;
+    w = sigmoid(my_z, rest);
+    if (renorm && __any(is_low(my_z))) w = sigmoid_times(my_z, max_of(my_z));
   } else {
     const float top = max_of(my_z);        // renormalised softmax: a softmax over the chosen
     const float base = renorm ? (top == -INFINITY ? 0.0f : top) : m0;
@@ -221,23 +247,38 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(const void* __restrict_
 #pragma unroll
   for (int i = 0; i < V; ++i) g[i] = z[i] == -INFINITY ? 0.0f : g[i];        // taken out: a gradient of any value counts nothing
   float m = -INFINITY;                       // over all experts, or the chosen ones
-#pragma unroll
-  for (int i = 0; i < V; ++i) m = fmaxf(m, (!renorm || n[i] > 0.0f) ? z[i] : -INFINITY);
-  m = max_of(m);
-  const float m0 = m == -INFINITY ? 0.0f : m;
-  float p[V], sum = 0.0f, dot = 0.0f;
+  bool low = false;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    if (SIGMOID) {
-      p[i] = 1.0f / (1.0f + expf(-z[i]));
+    m = fmaxf(m, (!renorm || n[i] > 0.0f) ? z[i] : -INFINITY);
+    low |= n[i] > 0.0f && is_low(z[i]);
+  }
+  m = max_of(m);
+  low = SIGMOID && renorm && __any(low);
+  const float m0 = m == -INFINITY ? 0.0f : m;
+  float p[V], rest[SIGMOID ? V : 1], sum = 0.0f, dot = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if constexpr (SIGMOID) {
+      p[i] = sigmoid(z[i], rest[i]);
+      if (low) p[i] = n[i] > 0.0f ? sigmoid_times(z[i], m) : 0.0f;
       sum += n[i] * p[i];
     } else {
       p[i] = renorm && n[i] == 0.0f ? 0.0f : expf(z[i] - m0);
       sum += renorm ? n[i] * p[i] : p[i];
     }
-    dot += g[i] * p[i];
+    if (!low) dot += g[i] * p[i];
   }
   sum = sum_of(sum);
+  if (low) {                                 // the ratios first: times the factor a gradient could leave the range
+    const float inv_sum = 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      p[i] *= inv_sum;
+      dot += g[i] * p[i];
+    }
+    sum = 1.0f;
+  }
   dot = sum_of(dot);
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
@@ -245,9 +286,8 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(const void* __restrict_
     const int e = lane + 64 * i;
     if (e >= E) continue;
     float d;
-    if (SIGMOID) {
-      const float ge = renorm ? (g[i] - n[i] * (dot * inv)) * inv : g[i];
-      d = ge * p[i] * (1.0f / (1.0f + expf(z[i])));        // 1 - p without cancellation
+    if constexpr (SIGMOID) {
+      d = (renorm ? (g[i] - n[i] * (dot * inv)) * (p[i] * inv) : g[i] * p[i]) * rest[i];
     } else {
       d = p[i] * inv * (g[i] - (renorm ? n[i] : 1.0f) * (dot * inv));
     }
@@ -333,7 +373,13 @@ __global__ __launch_bounds__(256) void router_bwd_rows_kernel(const void* __rest
 #pragma unroll
     for (int c = 0; c < 4; ++c) g[i][c] = z[i][c] == -INFINITY ? 0.0f : g[i][c];   // taken out: a gradient of any value counts nothing
   float m0 = -INFINITY;
-  if (!SIGMOID) {                            // the maximum over all experts, or the chosen ones
+  bool low = false;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) low |= n[i][c] > 0.0f && is_low(z[i][c]);
+  low = SIGMOID && renorm && row_max(low ? 1.0f : 0.0f) > 0.0f;
+  if (!SIGMOID || low) {                     // the maximum over all experts, or the chosen ones
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -341,21 +387,33 @@ __global__ __launch_bounds__(256) void router_bwd_rows_kernel(const void* __rest
     m0 = row_max(m0);
     if (m0 == -INFINITY) m0 = 0.0f;
   }
-  float p[V][4], sum = 0.0f, dot = 0.0f;
+  float p[V][4], rest[SIGMOID ? V : 1][4], sum = 0.0f, dot = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      if (SIGMOID) {
-        p[i][c] = 1.0f / (1.0f + expf(-z[i][c]));
+      if constexpr (SIGMOID) {
+        p[i][c] = sigmoid(z[i][c], rest[i][c]);
+        if (low) p[i][c] = n[i][c] > 0.0f ? sigmoid_times(z[i][c], m0) : 0.0f;
         sum += n[i][c] * p[i][c];
       } else {
         p[i][c] = renorm && n[i][c] == 0.0f ? 0.0f : expf(z[i][c] - m0);
         sum += renorm ? n[i][c] * p[i][c] : p[i][c];
       }
-      dot += g[i][c] * p[i][c];
+      if (!low) dot += g[i][c] * p[i][c];
     }
   sum = row_sum(sum);
+  if (low) {                                 // the ratios first: times the factor a gradient could leave the range
+    const float inv_sum = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        p[i][c] *= inv_sum;
+        dot += g[i][c] * p[i][c];
+      }
+    sum = 1.0f;
+  }
   dot = row_sum(dot);
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
   if (row >= T) return;
@@ -366,9 +424,8 @@ __global__ __launch_bounds__(256) void router_bwd_rows_kernel(const void* __rest
     float d[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      if (SIGMOID) {
-        const float ge = renorm ? (g[i][c] - n[i][c] * (dot * inv)) * inv : g[i][c];
-        d[c] = ge * p[i][c] * (1.0f / (1.0f + expf(z[i][c])));   // 1 - p without cancellation
+      if constexpr (SIGMOID) {
+        d[c] = (renorm ? (g[i][c] - n[i][c] * (dot * inv)) * (p[i][c] * inv) : g[i][c] * p[i][c]) * rest[i][c];
       } else {
         d[c] = p[i][c] * inv * (g[i][c] - (renorm ? n[i][c] : 1.0f) * (dot * inv));
       }

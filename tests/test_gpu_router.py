@@ -271,3 +271,40 @@ def test_gradients_of_masked_slots_take_no_part(E, score, renorm):
         got.append(host(dz))
     assert masked.sum() > 10 and np.isfinite(got[0]).all() and np.array_equal(got[0], got[1])
     assert (got[1][~np.isfinite(z)] == 0).all()
+
+
+# ------------------------------------------------------- logits far below zero
+LOW = [(9, 5, 3, -95.0, 4.0), (33, 64, 8, -150.0, 30.0), (18, 127, 16, -60.0, 40.0), (17, 256, 8, -250.0, 20.0), (5, 200, 4, -80.0, 12.0)]
+
+
+@pytest.mark.parametrize("T,E,k,mean,spread", LOW)
+@pytest.mark.parametrize("scale", [1.0, 2.5])
+def test_sigmoids_of_logits_far_below_zero(T, E, k, mean, spread, scale):
+    """Scores below float32's range still have a ratio: renormalised weights sum to the factor, and their gradient is
+    that of the ratio.  Tolerances as above: exponents of exact differences.  The oracle's own: it forms 1 - s from a
+    float64 s.  For z <= 0 that is off by 2^-53 of itself; for z > 0, s lies in [1/2, 1) and is off by 2^-54, so 1 - s
+    is off by 2^-54 in absolute terms, which every |g_j| carries twice at most (the diagonal and the renormalisation,
+    whose factors s / S are at most 1 where S >= s >= 1/2): 2^-52 of the gradients' sum in rows with such a logit."""
+    rng = np.random.default_rng([T, E])
+    z = (mean + spread * rng.standard_normal((T, E))).astype(np.float32)
+    z[0, : E // 2] = -np.inf
+    if T > 8:
+        z[3], z[4] = -np.inf, np.linspace(-20.0, -330.0, E).astype(np.float32)
+        z[5, ::2] += 60.0
+    zd = torch.from_numpy(z).cuda()
+    for bias in (None, (0.1 * rng.standard_normal(E)).astype(np.float32)):
+        for renorm in (False, True):
+            ids, w = run(zd, T, E, k, R.SIGMOID, None if bias is None else dev_f32(bias), renorm, scale)
+            oid, ow = R.router_topk(z, k, R.SIGMOID, bias, renorm, scale)
+            assert (host(ids) == oid).all()
+            assert (np.abs(host(w) - ow) <= 64 * U * np.abs(ow) + 1e-36).all(), (bias is None, renorm)
+            alive = np.isfinite(np.take_along_axis(z, oid.astype(np.int64), -1)).any(-1)
+            if renorm:
+                assert np.allclose(host(w)[alive].sum(-1), scale, rtol=1e-5) and (host(w)[~alive] == 0).all()
+            dw = rng.standard_normal((T, k)).astype(np.float32)
+            dz = torch.full_like(zd, float("nan"))
+            m.moe_router_topk_backward(zd, m.MOE_F32, E, ids, dev_f32(dw), T, E, k, R.SIGMOID, int(renorm), scale, dz, E)
+            o, mag = R.router_topk_backward(z, oid, dw, R.SIGMOID, renorm, scale)
+            above = (np.take_along_axis(z, oid.astype(np.int64), -1) > 0).any(-1, keepdims=True)
+            own = above * 2.0 ** -52 * np.abs(dw * scale).sum(-1, keepdims=True)
+            assert (np.abs(host(dz) - o) <= 160 * U * mag + own + 1e-36).all(), (bias is None, renorm)
