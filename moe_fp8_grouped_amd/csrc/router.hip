@@ -487,7 +487,7 @@ hipError_t launch_bwd(const void* z, int64_t ldl, const int32_t* ids, const floa
 
 int router_check(int dtype, int64_t ldl, int64_t T, int32_t E, int32_t k, int score, int renorm, float scale) {
   if (T < 0 || E <= 0 || E > kMaxE || k <= 0 || k > kMaxK || k > E || ldl < E) return MOE_ERR_SHAPE;
-  if (T > (int64_t{1} << 31)) return MOE_ERR_SHAPE;         // a wave a row: the grid stays below 2^31 workgroups
+  if (T > (int64_t{1} << 31)) return MOE_ERR_SHAPE;
   if (!(scale > 0.0f) || !(scale <= 3.402823466e38f)) return MOE_ERR_SHAPE;
   if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
   if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_UNSUPPORTED;
@@ -497,6 +497,10 @@ int router_check(int dtype, int64_t ldl, int64_t T, int32_t E, int32_t k, int sc
 
 }  // namespace
 }  // namespace moe
+
+// A launch takes fewer than 2^32 threads in a dimension (beyond that it runs a part of them without an error): rows by
+// parts that stay below with a wave a row.
+constexpr int64_t kRowsALaunch = int64_t{1} << 25;
 
 #define MOE_BY_V(CALL)                       \
   (E <= 64 ? CALL(1) : E <= 128 ? CALL(2) : E <= 256 ? CALL(4) : E <= 512 ? CALL(8) : CALL(16))
@@ -509,12 +513,19 @@ extern "C" int moe_router_topk(const void* logits, int logits_dtype, int64_t ldl
   if (T == 0) return MOE_OK;
   if (!logits || !expert_ids || !topk_weights) return MOE_ERR_NULL;
   hipStream_t st = static_cast<hipStream_t>(stream);
-#define MOE_B(V) moe::launch_topk<true, V>(logits, ldl, T, E, k, score, select_bias, renormalize, weight_scale, expert_ids, topk_weights, st)
-#define MOE_F(V) moe::launch_topk<false, V>(logits, ldl, T, E, k, score, select_bias, renormalize, weight_scale, expert_ids, topk_weights, st)
-  const hipError_t e = logits_dtype == MOE_BF16 ? MOE_BY_V(MOE_B) : MOE_BY_V(MOE_F);
+  for (int64_t t = 0; t < T; t += kRowsALaunch) {
+    const int64_t n = T - t < kRowsALaunch ? T - t : kRowsALaunch;
+    const void* z = static_cast<const char*>(logits) + t * ldl * (logits_dtype == MOE_BF16 ? 2 : 4);
+    int32_t* ids = expert_ids + t * k;
+    float* w = topk_weights + t * k;
+#define MOE_B(V) moe::launch_topk<true, V>(z, ldl, n, E, k, score, select_bias, renormalize, weight_scale, ids, w, st)
+#define MOE_F(V) moe::launch_topk<false, V>(z, ldl, n, E, k, score, select_bias, renormalize, weight_scale, ids, w, st)
+    const hipError_t e = logits_dtype == MOE_BF16 ? MOE_BY_V(MOE_B) : MOE_BY_V(MOE_F);
 #undef MOE_B
 #undef MOE_F
-  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    if (e != hipSuccess) return MOE_ERR_HIP;
+  }
+  return MOE_OK;
 }
 
 extern "C" int moe_router_topk_backward(const void* logits, int logits_dtype, int64_t ldl, const int32_t* expert_ids,
@@ -526,10 +537,18 @@ extern "C" int moe_router_topk_backward(const void* logits, int logits_dtype, in
   if (T == 0) return MOE_OK;
   if (!logits || !expert_ids || !dweights || !dlogits) return MOE_ERR_NULL;
   hipStream_t st = static_cast<hipStream_t>(stream);
-#define MOE_B(V) moe::launch_bwd<true, V>(logits, ldl, expert_ids, dweights, T, E, k, score, renormalize, weight_scale, dlogits, ldd, st)
-#define MOE_F(V) moe::launch_bwd<false, V>(logits, ldl, expert_ids, dweights, T, E, k, score, renormalize, weight_scale, dlogits, ldd, st)
-  const hipError_t e = logits_dtype == MOE_BF16 ? MOE_BY_V(MOE_B) : MOE_BY_V(MOE_F);
+  for (int64_t t = 0; t < T; t += kRowsALaunch) {
+    const int64_t n = T - t < kRowsALaunch ? T - t : kRowsALaunch, size = logits_dtype == MOE_BF16 ? 2 : 4;
+    const void* z = static_cast<const char*>(logits) + t * ldl * size;
+    void* dz = static_cast<char*>(dlogits) + t * ldd * size;
+    const int32_t* ids = expert_ids + t * k;
+    const float* dw = dweights + t * k;
+#define MOE_B(V) moe::launch_bwd<true, V>(z, ldl, ids, dw, n, E, k, score, renormalize, weight_scale, dz, ldd, st)
+#define MOE_F(V) moe::launch_bwd<false, V>(z, ldl, ids, dw, n, E, k, score, renormalize, weight_scale, dz, ldd, st)
+    const hipError_t e = logits_dtype == MOE_BF16 ? MOE_BY_V(MOE_B) : MOE_BY_V(MOE_F);
 #undef MOE_B
 #undef MOE_F
-  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    if (e != hipSuccess) return MOE_ERR_HIP;
+  }
+  return MOE_OK;
 }

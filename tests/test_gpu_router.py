@@ -308,3 +308,28 @@ def test_sigmoids_of_logits_far_below_zero(T, E, k, mean, spread, scale):
             above = (np.take_along_axis(z, oid.astype(np.int64), -1) > 0).any(-1, keepdims=True)
             own = above * 2.0 ** -52 * np.abs(dw * scale).sum(-1, keepdims=True)
             assert (np.abs(host(dz) - o) <= 160 * U * mag + own + 1e-36).all(), (bias is None, renorm)
+
+
+# ----------------------------------------------------------------- many tokens
+@pytest.mark.parametrize("E", [2, 130])
+def test_more_tokens_than_one_launch_takes(E):
+    """2^32 threads are the most a launch has: a wave a token, 2^26 of them."""
+    T = (1 << 26) + 5 if E == 2 else (1 << 26) + 1
+    z = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    z[:, 1] = 1.0
+    z[::7, 1] = -1.0
+    z[:, 2:] = -4.0
+    ids, w = torch.full((T, 1), -7, dtype=torch.int32, device="cuda"), torch.zeros(T, 1, device="cuda")
+    m.moe_router_topk(z, m.MOE_BF16, E, T, E, 1, R.SIGMOID, None, 0, 1.0, ids, w)
+    assert torch.equal(ids[:, 0], (z[:, 1] > 0).to(torch.int32))
+    p = torch.sigmoid(torch.tensor([0.0, 1.0], dtype=torch.float64)).tolist()
+    assert (w[ids == 0] - p[0]).abs().max().item() <= 64 * U and (w[ids == 1] - p[1]).abs().max().item() <= 64 * U
+    dz = torch.full_like(z, 3.0)
+    m.moe_router_topk_backward(z, m.MOE_BF16, E, ids, torch.ones_like(w), T, E, 1, R.SIGMOID, 0, 1.0, dz, E)
+    d = [v * (1 - v) for v in p]
+    for t in (0, 1, 7, (1 << 26) - 1, 1 << 26, T - 1):
+        e = int(ids[t, 0])
+        want = torch.zeros(E)
+        want[e] = d[e]
+        assert (dz[t].float().cpu() - want).abs().max().item() <= 2.0 ** -8 * d[e], t
+    assert int((dz != 0).sum()) == T
