@@ -615,7 +615,7 @@ extern "C" int moe_ffn_tokens(const void* x, int64_t ldx, const int32_t* expert_
   const bool mx = w_format == MOE_MX4;
   const int64_t unit = mx ? 32 : 16;
   if (T < 0 || k <= 0 || H <= 0 || I <= 0 || H % unit || I % unit || ldx < H || ldx % 8) return MOE_ERR_SHAPE;
-  if (E <= 0 || E > 1024 || group_offset < 0 || num_local_experts < 0 || group_offset + num_local_experts > E)
+  if (E <= 0 || E > 1024 || group_offset < 0 || num_local_experts < 0 || group_offset > E - num_local_experts)
     return MOE_ERR_SHAPE;
   if (H > (int64_t{1} << 20) || I > (int64_t{1} << 20)) return MOE_ERR_SHAPE;   // units, and offsets in 16 rows, stay below 2^31
   if (mx) {

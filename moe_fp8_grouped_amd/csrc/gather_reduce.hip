@@ -329,7 +329,7 @@ extern "C" int moe_gather_reduce_backward(const void* dout, const void* y, const
                                           int32_t num_local_experts, int64_t M_cap, void* dy, float* dw,
                                           uint8_t* dy_q, float* dy_scale, float* dy_amax, void* stream) {
   if (T < 0 || k <= 0 || k > 64 || N <= 0 || N % 8 || M_cap < 0) return MOE_ERR_SHAPE;
-  if (E <= 0 || E > 1024 || group_offset < 0 || num_local_experts < 0 || group_offset + num_local_experts > E)
+  if (E <= 0 || E > 1024 || group_offset < 0 || num_local_experts < 0 || group_offset > E - num_local_experts)
     return MOE_ERR_SHAPE;
   if (T * k > INT32_MAX - 1) return MOE_ERR_SHAPE;
   if (T == 0 && M_cap == 0) return MOE_OK;

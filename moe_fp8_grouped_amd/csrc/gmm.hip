@@ -1608,7 +1608,7 @@ int gmm_entry(const uint8_t* lhs, const float* lhs_scale, int lhs_scale_mode, co
   if (M < 0 || K <= 0 || N <= 0 || K % 16 || N % 16) return MOE_ERR_SHAPE;
   if (I8 && K > (int64_t{1} << 17)) return MOE_ERR_SHAPE;   // 127^2 * 2^17 < 2^31: the int32 sums stay exact
   if (E <= 0 || E > 1024 || group_offset < 0 || num_local_experts < 0 || num_local_experts > kMaxLocal ||
-      group_offset + num_local_experts > E)
+      group_offset > E - num_local_experts)
     return MOE_ERR_SHAPE;
   if (M > INT32_MAX - 1) return MOE_ERR_SHAPE;
   // the tile table of any split of M rows into El groups stays below 2^31 entries

@@ -806,7 +806,7 @@ extern "C" int moe_gmm_mx4(const uint8_t* lhs, int64_t ldl, const void* lhs_scal
   using moe::tile::kMaxLocal;
   if (M < 0 || K <= 0 || N <= 0 || K % 32 || N % 16) return MOE_ERR_SHAPE;
   if (E <= 0 || E > 1024 || group_offset < 0 || num_local_experts < 0 || num_local_experts > kMaxLocal ||
-      group_offset + num_local_experts > E)
+      group_offset > E - num_local_experts)
     return MOE_ERR_SHAPE;
   // row offsets inside a tile, and a group's weights' scale bytes, are 32-bit
   if (M > INT32_MAX - 1 || K > (1 << 22) || ldl > (1 << 23) || N > INT32_MAX || N * (K / 32) > INT32_MAX) return MOE_ERR_SHAPE;

@@ -549,7 +549,7 @@ int sort_check(const int32_t* expert_ids, int64_t T, int32_t k, int32_t E, int32
                int64_t M_cap, const int32_t* perm, const int32_t* inv_pos, const int32_t* group_sizes,
                const uint8_t* xs, const float* ss) {
   if (T < 0 || k <= 0 || k > 64 || E <= 0 || E > 1024) return MOE_ERR_SHAPE;
-  if (group_offset < 0 || num_local_experts < 0 || group_offset + num_local_experts > E) return MOE_ERR_SHAPE;
+  if (group_offset < 0 || num_local_experts < 0 || group_offset > E - num_local_experts) return MOE_ERR_SHAPE;
   if (M_cap < 0 || T * k > INT32_MAX - 1) return MOE_ERR_SHAPE;
   if (xscale_mode != MOE_SCALE_ROW_DYNAMIC && xscale_mode != MOE_SCALE_TENSOR_DYNAMIC &&
       xscale_mode != MOE_SCALE_TENSOR_STATIC)
@@ -609,7 +609,7 @@ extern "C" int moe_quantize_sort_by_expert(const void* x, int64_t T, int64_t H, 
                                            int32_t* group_sizes, uint8_t* xs, float* ss, float* scale,
                                            float* row_amax, void* ws, size_t ws_bytes, void* stream) {
   if (T < 0 || k <= 0 || k > 64 || E <= 0 || E > 1024) return MOE_ERR_SHAPE;
-  if (group_offset < 0 || num_local_experts < 0 || group_offset + num_local_experts > E) return MOE_ERR_SHAPE;
+  if (group_offset < 0 || num_local_experts < 0 || group_offset > E - num_local_experts) return MOE_ERR_SHAPE;
   if (M_cap < 0 || T * k > INT32_MAX - 1) return MOE_ERR_SHAPE;
   if (H <= 0 || H % 16) return MOE_ERR_SHAPE;
   if (scale_mode == MOE_SCALE_TENSOR_DYNAMIC) return MOE_ERR_UNSUPPORTED;   // needs the whole tensor first

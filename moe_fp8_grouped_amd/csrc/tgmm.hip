@@ -339,7 +339,7 @@ extern "C" int moe_tgmm_fp8(const uint8_t* lhs, const float* lhs_scale, int32_t 
                             void* out, void* ws, size_t ws_bytes, void* stream) {
   if (M < 0 || K <= 0 || N <= 0 || K % 16 || N % 16) return MOE_ERR_SHAPE;
   if (E <= 0 || E > 1024 || group_offset < 0 || num_local_experts < 0 ||
-      num_local_experts > moe::tile::kMaxLocal || group_offset + num_local_experts > E)
+      num_local_experts > moe::tile::kMaxLocal || group_offset > E - num_local_experts)
     return MOE_ERR_SHAPE;
   if (M > INT32_MAX - 1) return MOE_ERR_SHAPE;
   if (lhs_scale_len != 1 && lhs_scale_len != K) return MOE_ERR_UNSUPPORTED;
@@ -408,7 +408,7 @@ extern "C" int moe_sort_gather_transposed(const void* x, int x_dtype, float stat
   if (T < 0 || k <= 0 || k > 64 || H <= 0 || M < 0) return MOE_ERR_SHAPE;
   if (H % 256) return MOE_ERR_UNSUPPORTED;
   if (E <= 0 || E > 1024 || group_offset < 0 || num_local_experts < 0 ||
-      num_local_experts > moe::tile::kMaxLocal || group_offset + num_local_experts > E)
+      num_local_experts > moe::tile::kMaxLocal || group_offset > E - num_local_experts)
     return MOE_ERR_SHAPE;
   if (T * k > INT32_MAX - 1 || M > INT32_MAX - 1) return MOE_ERR_SHAPE;
   if (x_dtype != MOE_E4M3FN && x_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
@@ -445,7 +445,7 @@ extern "C" int moe_tgmm_fp8_xt(const uint8_t* xt, const float* lhs_scale, int32_
   if (M < 0 || K <= 0 || N <= 0) return MOE_ERR_SHAPE;
   if (K % 256 || N % 128) return MOE_ERR_UNSUPPORTED;
   if (E <= 0 || E > 1024 || group_offset < 0 || num_local_experts < 0 ||
-      num_local_experts > moe::tile::kMaxLocal || group_offset + num_local_experts > E)
+      num_local_experts > moe::tile::kMaxLocal || group_offset > E - num_local_experts)
     return MOE_ERR_SHAPE;
   if (M > INT32_MAX - 1) return MOE_ERR_SHAPE;
   if (lhs_scale_len != 1 && lhs_scale_len != K) return MOE_ERR_UNSUPPORTED;
