@@ -556,6 +556,12 @@ class MxRows:
         moe_quantize_rows_mx4(x, x_up, ldx, act, R, self.C, self.q, self.ld, self.scale, self.ld)
 
 
+def _expect(name, t, shape, dtypes, device, strided=False):
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or t.device != device or not (strided or t.is_contiguous()):
+        raise ValueError("%s must be a%s tensor %s of %s on %s" % (name, "" if strided else " contiguous", list(shape),
+                                                                  " or ".join(str(d) for d in dtypes), device))
+
+
 class RoutedFFN:
     """The gated expert layer of ``T`` tokens from the router's logits [T, E],
     expert weights in the 4-bit format:
@@ -577,6 +583,8 @@ class RoutedFFN:
 
     def __init__(self, x, logits, w0, w1, wo, k, rows=MOE_MX4, few=None, score=MOE_SCORE_SOFTMAX, renormalize=True,
                  weight_scale=1.0, select_bias=None, group_offset=0, m_cap=None):
+        if x.dim() != 2 or logits.dim() != 2 or w0.dim() != 3:
+            raise ValueError("x and logits have two dimensions, the weights three")
         dev = x.device
         self.x, self.logits, self.k, self.rows = x, logits, k, rows
         self.T, self.H = x.shape
@@ -585,6 +593,19 @@ class RoutedFFN:
         T, H, E, El = self.T, self.H, self.E, self.El
         if rows not in (MOE_MX4, MOE_E4M3FN):
             raise ValueError("rows must be MOE_MX4 or MOE_E4M3FN")
+        # the library sees addresses: what a buffer holds, and how much, is checked here
+        bf16, f32 = torch.bfloat16, torch.float32
+        _expect("x", x, (T, H), (bf16,), dev)
+        _expect("logits", logits, (T, E), (bf16, f32), dev)
+        _expect("w0", w0, (El, H, I), (bf16,), dev, strided=True)
+        _expect("w1", w1, (El, H, I), (bf16,), dev, strided=True)
+        _expect("wo", wo, (El, I, H), (bf16,), dev)
+        if select_bias is not None:
+            _expect("select_bias", select_bias, (E,), (f32,), dev)
+        if not 1 <= k <= min(E, 64):
+            raise ValueError("k must lie between 1 and the number of experts, at most 64")
+        if group_offset < 0 or group_offset + El > E:
+            raise ValueError("the local experts must be among the logits' experts")
         fits = T <= self.FEW_TOKENS and T * k <= self.FEW_ROWS
         if few and not fits:
             raise ValueError("the few-token layer takes up to 64 tokens and 1024 routed rows")
@@ -676,6 +697,7 @@ class RoutedFFN:
         also ``dy`` [m_cap, H], the sorted rows' gradient, and ``dw`` [T, k]."""
         if self.few:
             raise ValueError("the few-token layer keeps no expert outputs: build the layer with few=False")
+        _expect("dout", dout, (self.T, self.H), (torch.bfloat16,), self.x.device)
         if not hasattr(self, "dlogits"):
             self.dy = torch.empty((self.m_cap, self.H), dtype=torch.bfloat16, device=dout.device)
             self.dw = torch.empty((self.T, self.k), dtype=torch.float32, device=dout.device)
