@@ -681,6 +681,8 @@ class RoutedFFN:
         moe_gather_reduce(self.y, MOE_BF16, self.inv_pos, self.topk_w, self.T, self.k, self.H, MOE_BF16, self.out)
 
     def step(self):
+        if self.T == 0:                # no tokens: nothing to write
+            return
         self.route()
         if self.few:
             moe_ffn_tokens(self.x, self.H, self.ids, self.topk_w, self.T, self.k, self.H, self.I, self.E, self.g0, self.El,
@@ -702,6 +704,8 @@ class RoutedFFN:
             self.dy = torch.empty((self.m_cap, self.H), dtype=torch.bfloat16, device=dout.device)
             self.dw = torch.empty((self.T, self.k), dtype=torch.float32, device=dout.device)
             self.dlogits = torch.empty_like(self.logits)
+        if self.T == 0:
+            return
         moe_gather_reduce_backward(dout, self.y, self.inv_pos, self.topk_w, self.T, self.k, self.H, self.group_sizes,
                                    self.E, self.g0, self.El, self.m_cap, self.dy, self.dw, None, None, None)
         moe_router_topk_backward(self.logits, self.logits_dtype, self.E, self.ids, self.dw, self.T, self.E, self.k,

@@ -177,3 +177,15 @@ def test_on_another_stream_and_two_layers_at_once():
     torch.cuda.synchronize()
     for L in (A, B):
         assert np.array_equal(host(L.out), host(C.out)) and np.array_equal(host(L.y), host(C.y))
+
+
+@pytest.mark.parametrize("kw", [dict(few=True), dict(few=False), dict(few=False, rows=m.MOE_E4M3FN)], ids=str)
+def test_no_tokens(kw):
+    z, x, w = problem(3, 1, 8, 8, 64, 32)
+    L = layer(z[:0], x[:0], w, 2, **kw)
+    L.step()
+    torch.cuda.synchronize()
+    assert tuple(L.out.shape) == (0, 64)
+    if not L.few:
+        L.router_backward(dev_bf16(x[:0]))
+        assert tuple(L.dlogits.shape) == (0, 8)
