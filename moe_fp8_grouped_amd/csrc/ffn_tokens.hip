@@ -15,10 +15,13 @@
 // and the third adds each token's slots in slot order.
 //
 // Memory bounds it, then three launches and, in each, the routing, the first
-// loads and the tail.  Weights once at 5.2 TB/s, measured, and the first two
-// kernels' rates: one token of 7168, 8 experts of 2048 in e4m3 68 us, 76, 5.5
-// and 4.1 TB/s; 16 tokens of 2048, 8 of 64 experts of 768 in 4 bits 27, 51, 3.8
-// and 2.3; 64 such tokens in e4m3 58, 70, 5.5 and 4.0.
+// loads and the tail.  Weights once at 5.2 TB/s; a call among others, from
+// Python; the first two kernels in the trace, and their rates:
+//   one token of 7168, 8 e4m3 experts of 2048         68  67 us     40, 26 us  5.8, 4.6 TB/s
+//   16 tokens of 2048, 8 of 64 4-bit experts of 768   27  51        28, 22     3.4, 2.2
+//   64 such tokens in e4m3                            58  65 to 77  39, 25     5.1, 4.0
+// (Where two figures are compared below, both are calls as a graph, measured
+// side by side when the step was taken.)
 #include "mx4_common.hpp"
 #include "tile_common.hpp"
 
@@ -264,8 +267,8 @@ struct Loader {
       begin();
     }
   }
-  // AUX 2: not kept in the caches.  Weights that one pass reads are read once (one token e4m3 83 -> 75 us, 64 tokens
-  // 77 -> 69); those of an expert with more slots than a pass takes are read again.
+  // AUX 2: not kept in the caches.  Weights that one pass reads are read once (one token e4m3 75 us instead of
+  // 83, 64 tokens 69 instead of 77); those of an expert with more slots than a pass takes are read again.
   __device__ __forceinline__ void load() {
     if (seg.passes == 1)
       load<2>();
@@ -313,8 +316,8 @@ struct Loader {
 // whole 128-byte lines, each wave its own, kRing chunks ahead and on across
 // units and experts (16 KB a wave in flight).  Loaded to registers in the order
 // the matrix cores want them, by many small workgroups that each wait for
-// their own unit, the same layers took 113, 68 and 132 us where this takes the
-// times below.  The slots' rows are staged once an expert where they fit, else
+// their own unit, the same layers took 113, 68 and 132 us where this took 83,
+// 53 and 78.  The slots' rows are staged once an expert where they fit, else
 // by parts of the contraction.
 template <bool MX4, bool UP, int P, class Rows, class Finish>
 __device__ __forceinline__ void run_units(const Weights<UP>& m, Lds& sm, const FfnArgs& p, int first, int end, int units,

@@ -16,14 +16,15 @@
 //
 // Three kernels, all persistent, by format and size:
 //   4-bit rows, 256 x 256 tiles (run_wide): 8192 rows of 7168 by 32 groups of
-//     4096 columns 229 us, 2.1 PFLOP/s (128 rows a tile: 238; as run_tile: 259).
-//     Loads bound it: without its products and LDS reads it takes 207 us.
+//     4096 columns 218 us in the trace, 2.2 PFLOP/s (as calls 229; with 128
+//     rows a tile 238, as run_tile 259).  Loads bound it: without its products
+//     and LDS reads a call took 207 us.
 //   e4m3 rows, 128 x 256 tiles (run_tile, 4 column fragments a wave): 32768
-//     rows of 2048 by 64 groups of 1536 columns 132 us, 1.55 PFLOP/s (as
-//     256 x 256 tiles with the weights through LDS: 142).
+//     rows of 2048 by 64 groups of 1536 columns 122 us, 1.68 PFLOP/s (as calls
+//     132 then; as 256 x 256 tiles with the weights through LDS 142).
 //   fewer tiles than workgroups: 64-column tiles (run_tile, one column
-//     fragment a wave): 512 ragged rows of 2080 by 1040 columns 15 us, with
-//     256-column tiles 30; the two above would take 352 and 200.
+//     fragment a wave): 512 ragged rows of 2080 by 1040 columns 13.5 us (as
+//     calls 15; with 256-column tiles 30); the two above would take 352 and 200.
 // Weights kept out of the caches (they are read by two row tiles) cost the
 // first case 27 us.
 #include <type_traits>

@@ -108,9 +108,10 @@ __device__ __forceinline__ float sigmoid(float z, float& rest) {
 
 // One wave per row, expert e = lane + 64 i in register i.  Every choice is one
 // maximum over the wave (two for the bias's 64-bit keys), and ballots that find
-// its first expert.  8192 rows of 256 bf16 logits, k = 8: 10.2 us (with every
-// choice through LDS shuffles of key, expert and logit 25); what is left is
-// instructions, not the 0.9 us of bytes.
+// its first expert.  8192 rows of 256 bf16 logits, k = 8: 8.5 us in the
+// trace (as a graph of one call 10.2, where choices through LDS shuffles of key,
+// expert and logit took 25); what is left is instructions, not the 0.9 us of
+// bytes.
 template <bool BF16, int V, bool BIAS, bool SIGMOID>
 __global__ __launch_bounds__(256) void router_topk_kernel(const void* __restrict__ logits, int64_t ldl, int64_t T, int E,
                                                           int k, const float* __restrict__ bias, int renorm, float scale,
@@ -302,8 +303,9 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(const void* __restrict_
 // The same for up to 128 experts: sixteen lanes a row, four neighbouring
 // experts a lane and V times that, four rows a wave.  One wave a row spends its
 // instructions on idle lanes and on reductions over rows that hold little:
-// 32768 rows of 64 float32 logits, k = 8, 14.0 us against 9.6 (the bytes
-// alone 3.6; what is left is the launch and instructions).
+// 32768 rows of 64 float32 logits, k = 8, 14.0 us against 9.6 as graphs of one
+// call (8.4 in the trace; the bytes alone 3.6; what is left is the launch and
+// instructions).
 __device__ __forceinline__ float row_sum(float v) {   // over sixteen lanes, the same bits for each of them
   v += dpp<0xB1, 0xf>(0.0f, v);              // lane ^ 1, ^ 2, then halves and rows mirrored
   v += dpp<0x4E, 0xf>(0.0f, v);

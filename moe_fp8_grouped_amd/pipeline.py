@@ -569,8 +569,8 @@ class RoutedFFN:
       router    ids, weights = top-k of the logits
       few       out = the whole layer in one call, tokens unquantized
                 (up to 64 tokens and 1024 routed rows; with 64 experts of 2048 x
-                768, top-8, a step of 1, 16 and 64 tokens takes 30, 59 and 57 us,
-                the way below 43, 70 and 71)
+                768, top-8, a step of 1, 16 and 64 tokens takes 28, 60 and 69 us,
+                the way below 46, 81 and 84: graph replays, three layers in turn)
       otherwise x to rows (4-bit, or e4m3 with a scale a row) -> sort ->
                 [a | b] = gmm -> SiLU*mul to rows -> gmm -> gather-reduce
 
