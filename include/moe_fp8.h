@@ -542,8 +542,8 @@ int moe_silu_mul_backward(const void* a, const void* b, int64_t lda, const void*
  * token and their weights, from the token's logits z [E].
  *   scores   MOE_SCORE_SOFTMAX p_e = exp(z_e - m) / sum_f exp(z_f - m), or
  *            MOE_SCORE_SIGMOID p_e = 1 / (1 + exp(-z_e)), 0 for z_e below -700;
- *            renormalised weights are exact ratios down to there, also where
- *            every chosen p is below float32's range
+ *            renormalised weights are the ratios of such scores also where
+ *            every chosen one is below float32's range
  *   choice   the k largest logits (scores rise with them), or with
  *            select_bias the k largest p_e + select_bias[e], formed in 64
  *            bits; in descending order, equal ones to the lower expert

@@ -236,8 +236,9 @@ def test_a_token_alone_and_in_a_batch_of_many_units(fmt, dtype):
             blocks += [1, N]
     x = torch.randn(T, H, generator=gen, device="cuda").to(torch.bfloat16)
     ws = m.workspace(m.MOE_OP_FFN_TOKENS, T * 2, H, I, E)
-    for k in (1, 2):
-        ids = torch.rand(T, E, generator=gen, device="cuda").argsort(1)[:, :k].to(torch.int32).contiguous()
+    # experts by chance, and all tokens at two of them: passes of 16 slots, whose rows are staged by parts
+    for k, met in ((1, E), (2, E), (2, 2)):
+        ids = torch.rand(T, met, generator=gen, device="cuda").argsort(1)[:, :k].to(torch.int32).contiguous()
         tw = torch.rand(T, k, generator=gen, device="cuda")
 
         def call(rows):
