@@ -214,7 +214,7 @@ struct Loader {
   Lds& sm;
   Segment seg;
   int end, units, chunks, wave, lane;
-  int block_len;                                   // e4m3: elements of a K block (32-bit: a 64-bit division is most of this code)
+  int block_len;                                   // e4m3: elements of a K block (32-bit: 64-bit divisions were most of the code)
   int pass, job, c, step, q;                       // q: chunks loaded so far
   bool more;
   const uint8_t *w0, *w1, *s0, *s1;                // of the job
