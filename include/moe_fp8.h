@@ -61,6 +61,7 @@ extern "C" {
 #define MOE_F32 1
 #define MOE_E4M3FN 2
 #define MOE_MX4 3               /* microscaled 4-bit: see moe_quantize_rows_mx4 */
+#define MOE_E8M0 4              /* scale bytes s that stand for 2^(s - 127), 255 for NaN */
 
 /* activation-scale granularity */
 #define MOE_SCALE_ROW_DYNAMIC 0     /* one scale per row, from the row's absmax: [R] */
@@ -85,11 +86,15 @@ extern "C" {
 #define MOE_OP_QUANTIZE_WEIGHTS 5
 #define MOE_OP_GMM_MX4 6
 #define MOE_OP_FFN_TOKENS 7
+#define MOE_OP_GMM_B128 8
+#define MOE_OP_TGMM_B128 9
+#define MOE_OP_BALANCE 10
 
 /* bits of the sticky device-error word (first int32 of a workspace) */
 #define MOE_DEVERR_EXPERT_ID 1      /* an expert id outside [0, E) */
 #define MOE_DEVERR_GROUP_SIZE 2     /* a negative group size */
 #define MOE_DEVERR_ROWS 4           /* local rows exceed the row capacity */
+#define MOE_DEVERR_SEQUENCE 8       /* sequence offsets that decrease or leave the rows */
 
 /*
  * moe_quantize_rows -- absmax quantization of activations to e4m3fn.
@@ -708,12 +713,178 @@ int moe_ffn_tokens(const void* x, int64_t ldx, const int32_t* expert_ids, const 
                    void* stream);
 
 /*
+ * moe_quantize_rows_b128 -- rows to e4m3fn with a scale for every block of
+ * 128 elements (the last block of a row may be shorter): the format of the
+ * b128 calls.
+ *   scale    one e8m0 byte s a block, standing for 2^(s - 127): the smallest
+ *            power of two with block absmax <= 448 * 2^(s - 127), at least
+ *            2^-127; 127 for a block of zeros; 255 (NaN) for a block with an
+ *            element that is not finite: every element of it, and every
+ *            result of a product that it enters, is then NaN
+ *   codes    v / scale (exact) to the nearest e4m3fn value, ties to even; the
+ *            sign of zero is kept; 0 in a block of scale 255
+ *   x, x_up, ldx, act  [R, C] bf16, rows ldx elements apart, as in
+ *            moe_quantize_rows_strided (with MOE_ACT_SILU_MUL the matrix is
+ *            silu(x) * x_up in float32 by the same recipe).
+ *   q        [R, C] bytes out, rows ldq bytes apart.
+ *   scale    [R, ceil(C / 128)] bytes out, rows lds bytes apart.  q and scale
+ *            may be parts of one row (scale = q + C, ldq = lds), which one
+ *            gather (moe_sort_by_expert, which moves bytes) then moves; bytes
+ *            between the rows' parts are not written.
+ * C a multiple of 16, ldx >= C and a multiple of 8, ldq >= C and a multiple
+ * of 16, lds >= ceil(C / 128); x, x_up, q 16-byte aligned (MOE_ERR_SHAPE
+ * otherwise).  Needs no workspace.  Errors as in moe_quantize_rows_strided.
+ */
+int moe_quantize_rows_b128(const void* x, const void* x_up, int64_t ldx, int act, int64_t R, int64_t C, uint8_t* q,
+                           int64_t ldq, uint8_t* scale, int64_t lds, void* stream);
+
+/*
+ * moe_quantize_weights_b128 -- expert weights w [E, K, N] bf16 to e4m3fn with
+ * an e8m0 scale (as in moe_quantize_rows_b128) for every block of 128 by 128,
+ * in either or both orientations, in one pass:
+ *   q, scale       [E, N, K] codes and [E, ceil(K/128), 1, ceil(N/128)] scales:
+ *                  what moe_gmm_b128 reads for x W
+ *   qt, scale_t    [E, K, N] codes and [E, ceil(N/128), 1, ceil(K/128)] scales:
+ *                  what it reads for the input gradient dy W^T (contraction N)
+ * The two hold the same values.  A pair may be NULL, not both pairs.
+ * K and N multiples of 16; w, q, qt 16-byte aligned.  Needs no workspace.
+ * Errors: MOE_ERR_SHAPE, MOE_ERR_NULL; E = 0 returns MOE_OK.
+ */
+int moe_quantize_weights_b128(const void* w, int64_t E, int64_t K, int64_t N, uint8_t* q, uint8_t* scale, uint8_t* qt,
+                              uint8_t* scale_t, void* stream);
+
+/*
+ * moe_quantize_cols_b128 -- the rows of each local group to e4m3fn with a
+ * scale for every 128 of its rows and column, laid out column by column: the
+ * operand of the weight gradient, whose contraction runs along a group's
+ * rows.  With the local groups' sorted rows rows_off[g] .. rows_off[g] + m_g - 1
+ * and padded starts P_g = 128 * sum_{h<g} ceil(m_h / 128), as in
+ * moe_sort_gather_transposed:
+ *   qt[c, P_g + i]            code of V[rows_off[g] + i, c]   (i < m_g)
+ *                             0            (m_g <= i < 128 * ceil(m_g / 128))
+ *   scale_t[P_g / 128 + b, c] scale of rows 128 b .. of group g, column c
+ * scales and codes formed as in moe_quantize_rows_b128 along those rows.
+ * Columns (of qt) and rows (of scale_t) past the last group's padded end are
+ * not written.
+ *   V        the local sorted rows: with perm NULL, x itself, [M, C]; with
+ *            perm [T*k] (moe_sort_by_expert's), V[r] = x[perm[start + r] / k],
+ *            x [T, C] the tokens, start = sum of group_sizes[0 .. group_offset-1].
+ *   x, x_up, ldx, act as in moe_quantize_rows_b128.  T, k: as in the sort
+ *            (k is 1 to 64); without perm T is x's row count, at least M.
+ *   group_sizes, E, group_offset, num_local_experts: as in the sort.
+ *   M        local rows (rows of the weight gradient's operands).
+ *   qt       [C, moe_tgmm_xt_cols(M, E)] bytes, scale_t [cols / 128, C] bytes,
+ *            both 16-byte aligned.
+ *   ws       workspace of at least 256 bytes (the error word: negative sizes,
+ *            more local rows than M; a row index outside x is clamped).
+ * C a multiple of 16, M + 128 E <= 2^24.  Errors: MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_NULL, MOE_ERR_WORKSPACE.
+ */
+int moe_quantize_cols_b128(const void* x, const void* x_up, int64_t ldx, int act, int64_t T, int32_t k, const int32_t* perm,
+                           const int32_t* group_sizes, int32_t E, int32_t group_offset, int32_t num_local_experts,
+                           int64_t M, int64_t C, uint8_t* qt, uint8_t* scale_t, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_gmm_b128 -- moe_gmm_fp8 with a scale for every block of 128 of both
+ * operands: for local group g (rows as there)
+ *   out[r, c] = sum_b sx[r, b] * sw[g, b, c / 128] * sum_{k in block b} X[r, k] * W_g[k, c]
+ * accumulated in float32 by the scaled matrix cores, rounded once to
+ * out_dtype; rows past the last local group's are zero.
+ *   lhs      [M, K] e4m3fn, rows ldl bytes apart; lhs_scale [M, ceil(K/128)]
+ *            e8m0 bytes, rows lds apart (moe_quantize_rows_b128).  Scale rows
+ *            are read in whole pieces of 16 bytes, the last row's too.
+ *   rhs      [E_loc, N, K] e4m3fn; rhs_scale [E_loc, ceil(K/128), 1,
+ *            ceil(N/128)], of rhs_scale_dtype MOE_E8M0
+ *            (moe_quantize_weights_b128) or MOE_F32 (any float32: weights as
+ *            moe_quantize_weights or a checkpoint hold them in 128 x 128 blocks).
+ *   group_sizes .. num_local_experts, out, out_dtype as in moe_gmm_fp8.  One
+ *            group (E = 1, its size M) is a plain linear layer.
+ *   ws       workspace of moe_workspace_bytes(MOE_OP_GMM_B128, M, K, N, E).
+ * K and N multiples of 16, K <= 2^22, N * ceil(K/128) < 2^31; ldl a multiple
+ * of 16, K to 2^23; lds a multiple of 16, at least ceil(K/128); lhs,
+ * lhs_scale, rhs, out 16-byte aligned.  Errors as in moe_gmm_fp8.
+ */
+int moe_gmm_b128(const uint8_t* lhs, int64_t ldl, const uint8_t* lhs_scale, int64_t lds, const uint8_t* rhs,
+                 const void* rhs_scale, int rhs_scale_dtype, const int32_t* group_sizes, int32_t E, int32_t group_offset,
+                 int32_t num_local_experts, int64_t M, int64_t K, int64_t N, int out_dtype, void* out, void* ws,
+                 size_t ws_bytes, void* stream);
+
+/*
+ * moe_tgmm_b128 -- the weight gradient of moe_gmm_b128, both operands
+ * quantized along the rows of each group (moe_quantize_cols_b128):
+ *   out[g, k, c] = sum_b sx[b, k] * sy[b, c] * sum_{r in block b of group g} lhs_t[k, r] * rhs_t[c, r]
+ * accumulated in float32 by the scaled matrix cores; an empty local group
+ * gives zeros.
+ *   lhs_t    [K, cols] codes, lhs_scale [cols / 128, K]; rhs_t [N, cols],
+ *            rhs_scale [cols / 128, N]; cols = moe_tgmm_xt_cols(M, E).
+ *   group_sizes .. num_local_experts, M: as the operands were made with.
+ *   out      [E_loc, K, N], out_dtype MOE_F32 (default) or MOE_BF16.
+ *   ws       workspace of moe_workspace_bytes(MOE_OP_TGMM_B128, M, K, N, E).
+ * K and N multiples of 16, M + 128 E <= 2^24; all buffers 16-byte aligned.  Errors as
+ * in moe_tgmm_fp8.
+ */
+int moe_tgmm_b128(const uint8_t* lhs_t, const uint8_t* lhs_scale, const uint8_t* rhs_t, const uint8_t* rhs_scale,
+                  const int32_t* group_sizes, int32_t E, int32_t group_offset, int32_t num_local_experts, int64_t M,
+                  int64_t K, int64_t N, int out_dtype, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_balance_loss -- the router's balance loss of every sequence of a batch,
+ * and how often each expert was chosen.  With the shares p[t, e] of a token's
+ * scores (MOE_SCORE_SOFTMAX: the softmax of its logits; MOE_SCORE_SIGMOID:
+ * sigmoid(z_e) / sum_f sigmoid(z_f)), for sequence s of n tokens that have an
+ * expert, c[e] choices of expert e:
+ *   loss[s] = E / (k n^2) * sum_e c[e] * sum_t p[t, e]         (0 where n = 0)
+ * which is 1 where either is even over the experts.
+ *   logits, logits_dtype, ldl  [T, E] as in moe_router_topk.  A logit of -inf or
+ *            NaN, or at or below -1e30 (a mask of the type's lowest value), takes
+ *            its expert out for that token: no share, and no choice of it counts.
+ *            A token whose every logit is out (a padded one) is no token here.
+ *            +inf is not supported (its sequence's loss is unspecified).
+ *   expert_ids [T, k] int32 as moe_router_topk wrote them (an id outside [0, E)
+ *            does not count, one given twice counts twice).
+ *   seq_offsets [S + 1] int32, device: sequence s is the tokens
+ *            seq_offsets[s] .. seq_offsets[s+1] - 1 (it may be empty); rows
+ *            outside all sequences take no part.  NULL with S = 1: all T rows.
+ *            Offsets that decrease or leave [0, T] set MOE_DEVERR_SEQUENCE and
+ *            are clamped.
+ *   loss     [S] f32 out; counts [S, E] int32 out; tokens [S] int32 out: n.
+ *   ws       workspace of moe_workspace_bytes(MOE_OP_BALANCE, T, S, 0, E).
+ * The result's bits do not depend on the order in which the device runs.
+ * 1 <= E <= 1024, 1 <= k <= min(E, 64), 0 <= T <= 2^31 - 1, 1 <= S <= 2^24.
+ * Errors: MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_NULL, MOE_ERR_WORKSPACE.
+ */
+int moe_balance_loss(const void* logits, int logits_dtype, int64_t ldl, const int32_t* expert_ids, int64_t T, int32_t E,
+                     int32_t k, int score, const int32_t* seq_offsets, int32_t S, float* loss, int32_t* counts,
+                     int32_t* tokens, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_balance_loss_backward -- gradient of sum_s dloss[s] * loss[s] to the
+ * logits, the choices held fixed:
+ *   dz[t, e] = dloss[s] * E / (k n^2) * p_e * (c[e] - sum_f c[f] p_f) * r_e
+ * r_e = 1 for softmax, 1 - sigmoid(z_e) for sigmoid scores; 0 for experts
+ * taken out.
+ *   logits .. S as in the forward call; counts, tokens as it wrote them (a
+ *   data-parallel caller may have summed both over its ranks).
+ *   dloss    [S] f32.
+ *   accumulate 0: the rows of the sequences are written; 1: added, in float32,
+ *            to what dlogits holds (the router's own gradient), rounded once.
+ *   dlogits  [T, E], logits_dtype, rows ldd >= E elements apart; must not
+ *            overlap logits.  Rows outside all sequences are left as they are.
+ * Needs no workspace; offsets are clamped as in the forward call.
+ */
+int moe_balance_loss_backward(const void* logits, int logits_dtype, int64_t ldl, const int32_t* counts, const int32_t* tokens,
+                              const float* dloss, int64_t T, int32_t E, int32_t k, int score, const int32_t* seq_offsets,
+                              int32_t S, int accumulate, void* dlogits, int64_t ldd, void* stream);
+
+/*
  * moe_workspace_bytes -- workspace size (host out `bytes`) for `op` with
  * problem sizes d0, d1, d2 and E:
  *   MOE_OP_QUANTIZE_ROWS   d0 = R, d1 = C, d2 = scale_mode
  *   MOE_OP_SORT_BY_EXPERT  d0 = T*k
- *   MOE_OP_GMM, MOE_OP_TGMM, MOE_OP_GMM_MX4 d0 = M, d1 = K, d2 = N
+ *   MOE_OP_GMM, MOE_OP_TGMM, MOE_OP_GMM_MX4, MOE_OP_GMM_B128,
+ *   MOE_OP_TGMM_B128       d0 = M, d1 = K, d2 = N
  *   MOE_OP_FFN_TOKENS      d0 = T*k (at most 1024), d1 = H, d2 = I
+ *   MOE_OP_BALANCE         d0 = T, d1 = S
  *   others                 only the error word
  * Every size is a multiple of 256 bytes and at least 256.
  */

@@ -20,14 +20,14 @@ HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "moe_fp8.h")
 
 # constants mirrored from include/moe_fp8.h
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(6)
-MOE_DTYPE_DEFAULT, MOE_BF16, MOE_F32, MOE_E4M3FN, MOE_MX4 = -1, 0, 1, 2, 3
+MOE_DTYPE_DEFAULT, MOE_BF16, MOE_F32, MOE_E4M3FN, MOE_MX4, MOE_E8M0 = -1, 0, 1, 2, 3, 4
 MOE_SCALE_ROW_DYNAMIC, MOE_SCALE_TENSOR_DYNAMIC, MOE_SCALE_TENSOR_STATIC = 0, 1, 2
 MOE_SCALE_TENSOR_FROM_ROW_AMAX = 3
 MOE_ACT_NONE, MOE_ACT_SILU_MUL = 0, 1
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 (MOE_OP_QUANTIZE_ROWS, MOE_OP_SORT_BY_EXPERT, MOE_OP_GMM, MOE_OP_TGMM, MOE_OP_GATHER_REDUCE,
- MOE_OP_QUANTIZE_WEIGHTS, MOE_OP_GMM_MX4, MOE_OP_FFN_TOKENS) = range(8)
-MOE_DEVERR_EXPERT_ID, MOE_DEVERR_GROUP_SIZE, MOE_DEVERR_ROWS = 1, 2, 4
+ MOE_OP_QUANTIZE_WEIGHTS, MOE_OP_GMM_MX4, MOE_OP_FFN_TOKENS, MOE_OP_GMM_B128, MOE_OP_TGMM_B128, MOE_OP_BALANCE) = range(11)
+MOE_DEVERR_EXPERT_ID, MOE_DEVERR_GROUP_SIZE, MOE_DEVERR_ROWS, MOE_DEVERR_SEQUENCE = 1, 2, 4, 8
 MOE_SORT_NOALLOC_SCRATCH_BYTES = 2 << 20
 
 # C signatures: name -> (restype, argtypes)
@@ -72,6 +72,18 @@ SIGNATURES = {
     "moe_ffn_tokens": (_I, [_P, _I64, _P, _P, _I64, ctypes.c_int32, _I64, _I64, ctypes.c_int32, ctypes.c_int32,
                             ctypes.c_int32, _I, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, _P, ctypes.c_int32,
                             ctypes.c_int32, _I, _P, _P, _SZ, _P]),
+    "moe_quantize_rows_b128": (_I, [_P, _P, _I64, _I, _I64, _I64, _P, _I64, _P, _I64, _P]),
+    "moe_quantize_weights_b128": (_I, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
+    "moe_quantize_cols_b128": (_I, [_P, _P, _I64, _I, _I64, ctypes.c_int32, _P, _P, ctypes.c_int32, ctypes.c_int32,
+                                    ctypes.c_int32, _I64, _I64, _P, _P, _P, _SZ, _P]),
+    "moe_gmm_b128": (_I, [_P, _I64, _P, _I64, _P, _P, _I, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _I64, _I64,
+                          _I64, _I, _P, _P, _SZ, _P]),
+    "moe_tgmm_b128": (_I, [_P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _I64, _I64, _I64, _I, _P, _P,
+                           _SZ, _P]),
+    "moe_balance_loss": (_I, [_P, _I, _I64, _P, _I64, ctypes.c_int32, ctypes.c_int32, _I, _P, ctypes.c_int32, _P, _P, _P,
+                              _P, _SZ, _P]),
+    "moe_balance_loss_backward": (_I, [_P, _I, _I64, _P, _P, _P, _I64, ctypes.c_int32, ctypes.c_int32, _I, _P,
+                                       ctypes.c_int32, _I, _P, _I64, _P]),
     "moe_workspace_bytes": (_I, [_I, _I64, _I64, _I64, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
     "moe_debug_check": (_I, [_P, _P, ctypes.POINTER(ctypes.c_int32)]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
@@ -348,6 +360,56 @@ def moe_ffn_tokens(x, ldx, expert_ids, topk_weights, T, k, H, I, E, group_offset
                  group_offset, num_local_experts, w_format, _ptr(w01), _ptr(w01_scale), kb01, nb01, _ptr(wo),
                  _ptr(wo_scale), kbo, nbo, out_dtype, _ptr(out), _ptr(ws), _nbytes(ws),
                  _stream_here(stream, x, expert_ids, topk_weights, w01, w01_scale, wo, wo_scale, out, ws))
+
+
+def moe_quantize_rows_b128(x, x_up, ldx, act, R, C, q, ldq, scale, lds, stream=None):
+    """x, x_up, q, scale may be column slices of wider buffers (row strides ldx, ldx, ldq, lds)."""
+    return _call("moe_quantize_rows_b128", _ptr_rows(x, ldx), _ptr_rows(x_up, ldx), ldx, act, R, C, _ptr_rows(q, ldq), ldq,
+                 _ptr_rows(scale, lds), lds, _stream_here(stream, x, x_up, q, scale))
+
+
+def moe_quantize_weights_b128(w, E, K, N, q, scale, qt=None, scale_t=None, stream=None):
+    return _call("moe_quantize_weights_b128", _ptr(w), E, K, N, _ptr(q), _ptr(scale), _ptr(qt), _ptr(scale_t),
+                 _stream_here(stream, w, q, scale, qt, scale_t))
+
+
+def moe_quantize_cols_b128(x, x_up, ldx, act, T, k, perm, group_sizes, E, group_offset, num_local_experts, M, C, qt, scale_t,
+                           ws, stream=None):
+    """x, x_up may be column slices of wider buffers (row stride ldx)."""
+    return _call("moe_quantize_cols_b128", _ptr_rows(x, ldx), _ptr_rows(x_up, ldx), ldx, act, T, k, _ptr(perm),
+                 _ptr(group_sizes), E, group_offset, num_local_experts, M, C, _ptr(qt), _ptr(scale_t), _ptr(ws), _nbytes(ws),
+                 _stream_here(stream, x, x_up, perm, group_sizes, qt, scale_t, ws))
+
+
+def moe_gmm_b128(lhs, ldl, lhs_scale, lds, rhs, rhs_scale, rhs_scale_dtype, group_sizes, E, group_offset, num_local_experts,
+                 M, K, N, out_dtype, out, ws, stream=None):
+    """lhs and its scales may be column slices of wider buffers (row strides ldl, lds)."""
+    return _call("moe_gmm_b128", _ptr_rows(lhs, ldl), ldl, _ptr_rows(lhs_scale, lds), lds, _ptr(rhs), _ptr(rhs_scale),
+                 rhs_scale_dtype, _ptr(group_sizes), E, group_offset, num_local_experts, M, K, N, out_dtype, _ptr(out),
+                 _ptr(ws), _nbytes(ws), _stream_here(stream, lhs, lhs_scale, rhs, rhs_scale, group_sizes, out, ws))
+
+
+def moe_tgmm_b128(lhs_t, lhs_scale, rhs_t, rhs_scale, group_sizes, E, group_offset, num_local_experts, M, K, N, out_dtype, out,
+                  ws, stream=None):
+    return _call("moe_tgmm_b128", _ptr(lhs_t), _ptr(lhs_scale), _ptr(rhs_t), _ptr(rhs_scale), _ptr(group_sizes), E,
+                 group_offset, num_local_experts, M, K, N, out_dtype, _ptr(out), _ptr(ws), _nbytes(ws),
+                 _stream_here(stream, lhs_t, lhs_scale, rhs_t, rhs_scale, group_sizes, out, ws))
+
+
+def moe_balance_loss(logits, logits_dtype, ldl, expert_ids, T, E, k, score, seq_offsets, S, loss, counts, tokens, ws,
+                     stream=None):
+    """logits may be a column slice of a wider buffer (row stride ldl)."""
+    return _call("moe_balance_loss", _ptr_rows(logits, ldl), logits_dtype, ldl, _ptr(expert_ids), T, E, k, score,
+                 _ptr(seq_offsets), S, _ptr(loss), _ptr(counts), _ptr(tokens), _ptr(ws), _nbytes(ws),
+                 _stream_here(stream, logits, expert_ids, seq_offsets, loss, counts, tokens, ws))
+
+
+def moe_balance_loss_backward(logits, logits_dtype, ldl, counts, tokens, dloss, T, E, k, score, seq_offsets, S, accumulate,
+                              dlogits, ldd, stream=None):
+    """logits and dlogits may be column slices of wider buffers (row strides ldl, ldd)."""
+    return _call("moe_balance_loss_backward", _ptr_rows(logits, ldl), logits_dtype, ldl, _ptr(counts), _ptr(tokens),
+                 _ptr(dloss), T, E, k, score, _ptr(seq_offsets), S, accumulate, _ptr_rows(dlogits, ldd), ldd,
+                 _stream_here(stream, logits, counts, tokens, dloss, seq_offsets, dlogits))
 
 
 def moe_debug_check(ws, stream=None):

@@ -9,6 +9,9 @@ size_t gmm_ws_bytes();
 size_t tgmm_ws_bytes(int64_t M, int64_t K, int64_t N, int E);
 size_t gmm_mx4_ws_bytes(int64_t M, int64_t K);
 size_t ffn_tokens_ws_bytes(int64_t slots, int64_t H, int64_t I);
+size_t gmm_b128_ws_bytes();
+size_t tgmm_b128_ws_bytes();
+size_t balance_ws_bytes(int64_t T, int64_t S, int E);
 }  // namespace moe
 
 extern "C" int moe_workspace_bytes(int op, int64_t d0, int64_t d1, int64_t d2, int32_t E, size_t* bytes) {
@@ -37,6 +40,15 @@ extern "C" int moe_workspace_bytes(int op, int64_t d0, int64_t d1, int64_t d2, i
     case MOE_OP_FFN_TOKENS:
       if (d0 < 0 || d0 > 1024 || d1 < 0 || d1 > (1 << 20) || d2 < 0 || d2 > (1 << 20)) return MOE_ERR_SHAPE;
       *bytes = moe::ffn_tokens_ws_bytes(d0, d1, d2);
+      return MOE_OK;
+    case MOE_OP_GMM_B128:
+    case MOE_OP_TGMM_B128:
+      if (d0 < 0 || d1 < 0 || d2 < 0) return MOE_ERR_SHAPE;
+      *bytes = op == MOE_OP_GMM_B128 ? moe::gmm_b128_ws_bytes() : moe::tgmm_b128_ws_bytes();
+      return MOE_OK;
+    case MOE_OP_BALANCE:
+      if (d0 < 0 || d0 > INT32_MAX || d1 < 1 || d1 > (1 << 24) || E <= 0 || E > 1024) return MOE_ERR_SHAPE;
+      *bytes = moe::balance_ws_bytes(d0, d1, E);
       return MOE_OK;
     case MOE_OP_GATHER_REDUCE:
     case MOE_OP_QUANTIZE_WEIGHTS:
@@ -67,4 +79,4 @@ extern "C" const char* moe_status_string(int status) {
   }
 }
 
-extern "C" int moe_version(void) { return 200; }
+extern "C" int moe_version(void) { return 300; }

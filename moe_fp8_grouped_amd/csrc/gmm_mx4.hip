@@ -30,11 +30,12 @@
 #include <type_traits>
 
 #include "mx4_common.hpp"
-#include "tile_common.hpp"
+#include "stage_common.hpp"
 
 namespace moe {
 namespace {
 using namespace tile;
+using namespace stage;
 using mx4::quad_exchange;
 
 // First operand e2m1 (format 4); second e4m3 (0) or e2m1 (4).
@@ -66,10 +67,6 @@ struct Mx4Args {
   int tile_rows;               // rows a tile holds at most
 };
 
-typedef __attribute__((address_space(3))) void lds_void;
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-typedef int v4i __attribute__((ext_vector_type(4)));
-
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kRows = 128;                       // rows a tile holds at most
 constexpr int kStages = 3;
@@ -80,37 +77,6 @@ constexpr int kDesc = 64;                        // tiles decoded at a time
 // use eight slots, so a fragment read (16 rows, served 8 lanes at a time) is
 // free of bank conflicts.
 __device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
-
-constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
-
-// No memory access crosses: the order of the loads below is what the waits count.
-__device__ __forceinline__ void order() { asm volatile("" ::: "memory"); }
-__device__ __forceinline__ void step_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
-// A lane number that the compiler cannot carry from one use to the next: what
-// follows from it is formed again where it is needed instead of being held in
-// registers through the loop.
-__device__ __forceinline__ int opaque(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_u8*)p));
-}
-
-// Buffer over `bytes` bytes from p (uniform): loads take a lane offset and a
-// uniform one, so a lane keeps 32 bits of address however far the loop goes.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* p, uint32_t bytes) {
-  const uint64_t b = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32));
-  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0,
-                                           __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
-}
-__device__ __forceinline__ uint4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t add) {
-  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, add, 0));
-}
 
 // LDS reads that are complete on return.  One asm block each: the regions are
 // filled by direct loads that the caller has waited for, and for a plain read
@@ -176,10 +142,6 @@ __device__ __forceinline__ void read_scales(uint32_t a, uint32_t (&s)[CF]) {
   else
     asm volatile("ds_read_u8 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(s[0]) : "v"(a) : "memory");
 }
-
-// A group of m rows: as few tiles as hold them, evenly filled with blocks of 16.
-__device__ __forceinline__ int row_tiles(int m, int most) { return (m + most - 1) / most; }
-__device__ __forceinline__ int tile_frags(int m, int nb) { return ((m + 15) / 16 + nb - 1) / nb; }
 
 struct Tile {
   int64_t row0, col0;
@@ -506,11 +468,6 @@ static_assert(sizeof(WideLds) <= 160 * 1024, "LDS of a CU");
 // four rows, 16 apart.
 __device__ __forceinline__ int xswz64(int r) { return (r >> 1) & 3; }
 __device__ __forceinline__ int wswz64(int r) { return ((r >> 1) & 1) + 2 * ((r >> 4) & 1); }
-
-template <class T>
-__device__ __forceinline__ T lds_read(uint32_t a) {   // (an address without a provenance: see run_wide)
-  return *(const __attribute__((address_space(3))) T*)(uintptr_t)(a);
-}
 
 // One tile, up to 32 MI rows by 256 columns: two waves by four, each 16 MI rows by 64 columns.  Rows and weights
 // both go to LDS by direct loads (neighbouring lanes on one row), NST - 1 stages ahead.  The fragments are plain LDS
