@@ -777,7 +777,7 @@ int moe_quantize_weights_b128(const void* w, int64_t E, int64_t K, int64_t N, ui
  *            both 16-byte aligned.
  *   ws       workspace of at least 256 bytes (the error word: negative sizes,
  *            more local rows than M; a row index outside x is clamped).
- * C a multiple of 16, M + 128 E <= 2^24.  Errors: MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED,
+ * C a multiple of 16, M + 128 E <= 2^23.  Errors: MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED,
  * MOE_ERR_NULL, MOE_ERR_WORKSPACE.
  */
 int moe_quantize_cols_b128(const void* x, const void* x_up, int64_t ldx, int act, int64_t T, int32_t k, const int32_t* perm,
@@ -800,7 +800,7 @@ int moe_quantize_cols_b128(const void* x, const void* x_up, int64_t ldx, int act
  *   group_sizes .. num_local_experts, out, out_dtype as in moe_gmm_fp8.  One
  *            group (E = 1, its size M) is a plain linear layer.
  *   ws       workspace of moe_workspace_bytes(MOE_OP_GMM_B128, M, K, N, E).
- * K and N multiples of 16, K <= 2^22, N * ceil(K/128) < 2^31; ldl a multiple
+ * K and N multiples of 16 and at most 2^22, N * ceil(K/128) < 2^31; ldl a multiple
  * of 16, K to 2^23; lds a multiple of 16, at least ceil(K/128); lhs,
  * lhs_scale, rhs, out 16-byte aligned.  Errors as in moe_gmm_fp8.
  */
@@ -820,7 +820,7 @@ int moe_gmm_b128(const uint8_t* lhs, int64_t ldl, const uint8_t* lhs_scale, int6
  *   group_sizes .. num_local_experts, M: as the operands were made with.
  *   out      [E_loc, K, N], out_dtype MOE_F32 (default) or MOE_BF16.
  *   ws       workspace of moe_workspace_bytes(MOE_OP_TGMM_B128, M, K, N, E).
- * K and N multiples of 16, M + 128 E <= 2^24; all buffers 16-byte aligned.  Errors as
+ * K and N multiples of 16 and at most 2^22, M + 128 E <= 2^23; all buffers 16-byte aligned.  Errors as
  * in moe_tgmm_fp8.
  */
 int moe_tgmm_b128(const uint8_t* lhs_t, const uint8_t* lhs_scale, const uint8_t* rhs_t, const uint8_t* rhs_scale,

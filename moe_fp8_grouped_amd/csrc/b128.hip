@@ -319,7 +319,7 @@ extern "C" int moe_quantize_cols_b128(const void* x, const void* x_up, int64_t l
                                       size_t ws_bytes, void* stream) {
   if (M < 0 || C <= 0 || C % 16 || C > INT32_MAX || ldx < C || ldx % 8 || T < 0 || k < 1 || k > 64) return MOE_ERR_SHAPE;
   if (E <= 0 || E > 1024 || group_offset < 0 || num_local_experts < 0 || group_offset > E - num_local_experts) return MOE_ERR_SHAPE;
-  if (M > (int64_t{1} << 24) || M + 128 * static_cast<int64_t>(E) > (int64_t{1} << 24)) return MOE_ERR_SHAPE;
+  if (M > (int64_t{1} << 23) || M + 128 * static_cast<int64_t>(E) > (int64_t{1} << 23)) return MOE_ERR_SHAPE;
   if (T > INT32_MAX || (!perm && T < M)) return MOE_ERR_SHAPE;
   if (act != MOE_ACT_NONE && act != MOE_ACT_SILU_MUL) return MOE_ERR_UNSUPPORTED;
   if (act == MOE_ACT_NONE && x_up) return MOE_ERR_UNSUPPORTED;

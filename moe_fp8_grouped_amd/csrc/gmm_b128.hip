@@ -55,6 +55,15 @@ __device__ __forceinline__ void store4(void* out, int64_t at, const v4f& v) {
     *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
+// Rows past the last group's are zero.
+template <bool OUT_BF16, int THREADS>
+__device__ __forceinline__ void zero_rows(const B128Args& p, int64_t n_rows) {
+  const int64_t bytes = (p.M - n_rows) * p.N * (OUT_BF16 ? 2 : 4);
+  uint8_t* z = static_cast<uint8_t*>(p.out) + n_rows * p.N * (OUT_BF16 ? 2 : 4);
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x) * 16; i < bytes; i += static_cast<int64_t>(gridDim.x) * THREADS * 16)
+    *reinterpret_cast<uint4*>(z + i) = make_uint4(0, 0, 0, 0);
+}
+
 // ------------------------------------------------------------ 16 x 16 tiles
 // A workgroup takes one tile, the contraction's blocks dealt out to its waves,
 // whose sums are added in wave order.
@@ -148,17 +157,350 @@ __global__ __launch_bounds__(64 * kSplit) void b128_small_kernel(const B128Args 
         store4<OUT_BF16>(p.out, (TG ? static_cast<int64_t>(g) * p.K + row0 + l15 : row0 + l15) * p.N + col0 + 4 * grp, acc);
     }
   }
-  if constexpr (!TG) {                             // rows past the last group's are zero
-    const int64_t n_rows = sm.gt.rows_off[p.El], bytes = (p.M - n_rows) * p.N * (OUT_BF16 ? 2 : 4);
-    uint8_t* z = static_cast<uint8_t*>(p.out) + n_rows * p.N * (OUT_BF16 ? 2 : 4);
-    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 64 * kSplit + tid) * 16; i < bytes; i += static_cast<int64_t>(gridDim.x) * 64 * kSplit * 16)
-      *reinterpret_cast<uint4*>(z + i) = make_uint4(0, 0, 0, 0);
+  if constexpr (!TG) zero_rows<OUT_BF16, 64 * kSplit>(p, sm.gt.rows_off[p.El]);
+}
+
+// ---------------------------------------------------------------- wide tiles
+// 256 x 256 results a workgroup of eight waves, two by four, each 16 MI rows by
+// 64 columns.  A stage is one block of the contraction, 128 bytes of every row
+// of both operands: whole lines, by direct loads to LDS, the next stage's
+// issued when this one's are there.  The stream runs on from tile to tile: the next
+// tile's first stage is on its way before this one's results are stored.
+constexpr int kWideThreads = 512, kWideRows = 256, kWideCols = 256, kWindow = 16, kDesc = 64;
+
+struct WideLds {
+  uint8_t x[2][kWideRows * 128];
+  uint8_t w[2][kWideCols * 128];
+  uint8_t xs[2][kWideRows * kWindow];              // scales of a window of 16 blocks: gmm a row's 16 bytes, tgmm a block's 256
+  uint8_t ws[2][kWideCols * kWindow];              // gmm: 16 blocks by 2, a dword each
+  int4 desc[kDesc];                                // first row, column tile, group, rows
+  int2 more[kDesc];                                // blocks, first block
+};
+static_assert(sizeof(WideLds) <= 160 * 1024, "LDS of a CU");
+
+// Slot of 16-byte chunk c of a staged row r: c ^ swizzle(r), so that the eight rows that neighbouring lanes read lie
+// in eight slots: runs of rows, or (bf16 results) lanes l%16 at rows 8 (l%16 / 4) + l%4.
+__device__ __forceinline__ int swz_run(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+__device__ __forceinline__ int swz_quads(int r) { return (r & 3) + 4 * ((r >> 3) & 1); }
+// First column in a wave's 64 of what lane l%16 = n supplies as weight row of fragment f: output lanes l/16 then hold
+// columns whose stores make runs of 64 bytes, eight bf16 of fragments 2 h and 2 h + 1, or four float32 of one.
+template <bool OUT_BF16>
+__device__ __forceinline__ constexpr int frag_col(int f, int n) {
+  return OUT_BF16 ? 32 * (f >> 1) + 8 * (n >> 2) + 4 * (f & 1) + (n & 3) : 16 * f + n;
+}
+
+struct WideTile {
+  int64_t row0, col0;                              // (tgmm: in the group's result)
+  int g, rows, steps, blk0;
+};
+
+__device__ __forceinline__ WideTile wide_tile(const WideLds& sm, int i) {
+  const v4i d = lds_read<v4i>(lds_addr(sm.desc) + 16 * i);
+  const v2i m = lds_read<v2i>(lds_addr(sm.more) + 8 * i);
+  WideTile t;
+  t.row0 = __builtin_amdgcn_readfirstlane(d[0]);
+  t.col0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(d[1])) * kWideCols;
+  t.g = __builtin_amdgcn_readfirstlane(d[2]);
+  t.rows = __builtin_amdgcn_readfirstlane(d[3]);
+  t.steps = __builtin_amdgcn_readfirstlane(m[0]);
+  t.blk0 = __builtin_amdgcn_readfirstlane(m[1]);
+  return t;
+}
+
+// What the loads of a tile go by.
+template <Kind KIND, bool OUT_BF16>
+struct WideSource {
+  __amdgpu_buffer_rsrc_t x, w;
+  WideTile t;
+
+  __device__ __forceinline__ void set(const B128Args& p, const WideTile& tile) {
+    t = tile;
+    const uint32_t cols = static_cast<uint32_t>(min(p.N - t.col0, static_cast<int64_t>(kWideCols)));
+    if constexpr (KIND == kTgmm) {
+      const uint32_t len = 128u * t.steps, ld = static_cast<uint32_t>(p.ldx);
+      const int64_t at = 128 * static_cast<int64_t>(t.blk0);
+      x = buffer(p.x + t.row0 * p.ldx + at, (t.rows - 1) * ld + len);
+      w = buffer(p.w + t.col0 * p.ldx + at, (cols - 1) * ld + len);
+    } else {
+      const uint32_t K = static_cast<uint32_t>(p.K);
+      x = buffer(p.x + t.row0 * p.ldx, (t.rows - 1) * static_cast<uint32_t>(p.ldx) + K);
+      w = buffer(p.w + (static_cast<int64_t>(t.g) * p.N + t.col0) * p.K, cols * K);
+    }
   }
+
+  // Stage s to buffer b; lane l fills slot l%8 of rows 8 wave + l/8 (+ 64 i).  Rows past the tile's, columns past N and
+  // chunks past K lie outside the buffers: zeros.
+  __device__ __forceinline__ void load(const B128Args& p, WideLds& sm, int s, int b, int wave, int lane) const {
+    const int r = 8 * wave + (lane >> 3);
+    const uint32_t ldx = static_cast<uint32_t>(p.ldx), ldw = KIND == kTgmm ? ldx : static_cast<uint32_t>(p.K);
+    const uint32_t xc = 16 * ((lane & 7) ^ swz_run(r)), wc = 16 * ((lane & 7) ^ (OUT_BF16 ? swz_quads(r) : swz_run(r)));
+    uint32_t xo = r * ldx + xc, wo = r * ldw + wc;
+    if (KIND != kTgmm && 128 * s + 128 > p.K) {
+      const uint32_t left = static_cast<uint32_t>(p.K) - 128u * s;
+      xo = xc < left ? xo : 0x80000000u;
+      wo = wc < left ? wo : 0x80000000u;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(w, (lds_void*)(sm.w[b] + (64 * i + 8 * wave) * 128), 16, wo, 128u * s + 64 * i * ldw, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (64 * i + 8 * wave < t.rows)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(x, (lds_void*)(sm.x[b] + (64 * i + 8 * wave) * 128), 16, xo, 128u * s + 64 * i * ldx, 0, 0);
+  }
+
+  // Scales of blocks 16 win .. to buffer b.  (Lanes past the tile or the contraction fetch what is there of its last.)
+  __device__ __forceinline__ void load_scales(const B128Args& p, WideLds& sm, int win, int b, int wave, int lane) const {
+    if constexpr (KIND == kTgmm) {                 // [block][K or N]: lanes 16 j .. 16 j + 15 the 256 bytes of block 4 wave + j
+      const int blk = kWindow * win + 4 * (wave & 3) + (lane >> 4);
+      const int64_t n = wave < 4 ? p.K : p.N, c = (wave < 4 ? t.row0 : t.col0) + 16 * (lane & 15);
+      const uint8_t* src = (wave < 4 ? p.xs : static_cast<const uint8_t*>(p.ws)) +
+                           (t.blk0 + min(blk, t.steps - 1)) * n + min(c, n - 16);
+      uint8_t* dst = (wave < 4 ? sm.xs[b] : sm.ws[b]) + 1024 * (wave & 3);
+      __builtin_amdgcn_global_load_lds(src, (lds_void*)dst, 16, 0, 0);
+    } else {
+      if (lane < 32 && 32 * wave < t.rows) {
+        const int64_t row = t.row0 + min(32 * wave + lane, t.rows - 1);
+        __builtin_amdgcn_global_load_lds(p.xs + row * p.lds + kWindow * win, (lds_void*)(sm.xs[b] + 512 * wave), 16, 0, 0);
+      }
+      if (wave == 7 && lane < 32) {                // block win * 16 + lane / 2, column block lane & 1 of the tile's two
+        const int64_t nb = (p.N + 127) / 128;
+        const int64_t c = min(t.col0 / 128 + (lane & 1), nb - 1);
+        const int64_t at = (static_cast<int64_t>(t.g) * t.steps + min(kWindow * win + (lane >> 1), t.steps - 1)) * nb + c;
+        const uint8_t* src = static_cast<const uint8_t*>(p.ws) + (KIND == kGmmF32 ? 4 * at : at);
+        if (KIND == kGmmE8M0) src -= reinterpret_cast<uintptr_t>(src) & 3;         // the dword that holds the byte
+        __builtin_amdgcn_global_load_lds(src, (lds_void*)sm.ws[b], 4, 0, 0);
+      }
+    }
+  }
+};
+
+template <Kind KIND, bool OUT_BF16, int MI>
+__device__ __forceinline__ void wide_stage(const B128Args& p, const WideTile& t, int s, int b, int win, int wave, int lane,
+                                           const WideLds& sm, v4f (&acc)[MI][4]) {
+  const int l15 = lane & 15, grp = lane >> 4, wr = wave >> 2, wc = wave & 3;
+  const int xr = 16 * MI * wr + l15, wrow = 64 * wc + frag_col<OUT_BF16>(0, l15);
+  const uint32_t xa = lds_addr(sm.x[0]) + b * static_cast<uint32_t>(sizeof(sm.x[0])) + xr * 128 + 16 * (grp ^ swz_run(l15));
+  const uint32_t wa = lds_addr(sm.w[0]) + b * static_cast<uint32_t>(sizeof(sm.w[0])) + wrow * 128 +
+                      16 * (grp ^ (OUT_BF16 ? swz_quads(wrow) : swz_run(wrow)));
+  const uint32_t xsb = lds_addr(sm.xs[0]) + win * static_cast<uint32_t>(sizeof(sm.xs[0]));
+  const uint32_t wsb = lds_addr(sm.ws[0]) + win * static_cast<uint32_t>(sizeof(sm.ws[0]));
+  const int sb = s & (kWindow - 1);
+  v8i w[4];
+  uint32_t wsc[4];
+  float wf = 0.0f;
+#pragma unroll
+  for (int f = 0; f < 4; ++f) {
+    const uint32_t at = frag_col<OUT_BF16>(f, 0) * 128;
+    w[f] = frag(__builtin_bit_cast(uint4, lds_read<v4i>(wa + at)), __builtin_bit_cast(uint4, lds_read<v4i>((wa ^ 64u) + at)));
+    if (KIND == kTgmm) wsc[f] = lds_read<uint8_t>(wsb + 256 * sb + wrow + frag_col<OUT_BF16>(f, 0));
+  }
+  if constexpr (KIND == kGmmE8M0) {
+    const int64_t nb = (p.N + 127) / 128, c = min(t.col0 / 128 + (wc >> 1), nb - 1);
+    const int64_t at = (static_cast<int64_t>(t.g) * t.steps + s) * nb + c;
+    const uint32_t byte = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.ws) + at) & 3;
+    wsc[0] = wsc[1] = wsc[2] = wsc[3] = lds_read<uint8_t>(wsb + 8 * sb + 4 * (wc >> 1) + byte);
+  }
+  if constexpr (KIND == kGmmF32) wf = lds_read<float>(wsb + 8 * sb + 4 * (wc >> 1));
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const v8i x = frag(__builtin_bit_cast(uint4, lds_read<v4i>(xa + 2048 * i)), __builtin_bit_cast(uint4, lds_read<v4i>((xa ^ 64u) + 2048 * i)));
+    const uint32_t xs = KIND == kTgmm ? lds_read<uint8_t>(xsb + 256 * sb + xr + 16 * i) : lds_read<uint8_t>(xsb + (xr + 16 * i) * kWindow + sb);
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      if constexpr (KIND == kGmmF32)
+        acc[i][f] += wf * mfma_scaled(w[f], 127, x, xs, v4f{0.f, 0.f, 0.f, 0.f});
+      else
+        acc[i][f] = mfma_scaled(w[f], wsc[f], x, xs, acc[i][f]);
+    }
+  }
+}
+
+// Every store is issued whatever the tile holds (rows past it, columns past N lie outside the buffer), so that their
+// number is known to the waits.
+template <bool OUT_BF16, int MI>
+__device__ __forceinline__ void wide_store(const B128Args& p, const WideTile& t, int64_t out_row0, int wave, int lane, const v4f (&acc)[MI][4]) {
+  constexpr int B = OUT_BF16 ? 2 : 4;
+  const int l15 = lane & 15, grp = lane >> 4, wr = wave >> 2, wc = wave & 3;
+  const uint32_t ld = static_cast<uint32_t>(p.N) * B;
+  const int64_t c = t.col0 + 64 * wc;
+  uint8_t* base = static_cast<uint8_t*>(p.out) + (out_row0 + 16 * MI * wr) * p.N * B + c * B;
+  const int rows = t.rows - 16 * MI * wr;          // the wave's rows (or none)
+  const int64_t left = p.N - c;                    // its columns
+  const __amdgpu_buffer_rsrc_t o = buffer(base, rows > 0 && left > 0 ? (rows - 1) * ld + static_cast<uint32_t>(min(left, static_cast<int64_t>(64))) * B : 0u);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const uint32_t row = (16 * i + l15) * ld;
+    if (OUT_BF16) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        v4u32 v;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const v4f& a = acc[i][2 * h + (q >> 1)];
+          v[q] = f32_to_bf16(a[2 * (q & 1)]) | static_cast<uint32_t>(f32_to_bf16(a[2 * (q & 1) + 1])) << 16;
+        }
+        const int col = 32 * h + 8 * grp;
+        __builtin_amdgcn_raw_buffer_store_b128(v, o, col < left ? row + 2 * col : 0xf0000000u, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int col = 16 * f + 4 * grp;
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, acc[i][f]), o, col < left ? row + 4 * col : 0xf0000000u, 0, 0);
+      }
+    }
+  }
+}
+
+// One tile from the stream: `src` holds it, its first stage is loaded (or on its way) in buffer b; `next` (if there is one)
+// the tile that follows.  `behind`: its first stage was issued before the last tile's stores.
+template <Kind KIND, bool OUT_BF16, int MI>
+__device__ __forceinline__ void run_wide(const B128Args& p, WideLds& sm, WideSource<KIND, OUT_BF16>& src, const WideTile& next,
+                                         bool has_next, int& b, int& win, bool behind) {
+  constexpr int kStores = (OUT_BF16 ? 2 : 4) * MI;
+  const int tid = opaque(threadIdx.x);
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const WideTile t = src.t;
+  v4f acc[MI][4];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int f = 0; f < 4; ++f) acc[i][f] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma clang loop unroll(disable)
+  for (int s = 0; s < t.steps; ++s) {
+    if (KIND == kTgmm && s == 0 && behind)
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(kStores));       // this wave's loads of stage s are there, the stores may be on their way
+    else
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    step_barrier();                                          // every wave's are; the other buffer is read
+    order();
+    if (s + 1 < t.steps) {
+      if ((s + 1) % kWindow == 0) src.load_scales(p, sm, (s + 1) / kWindow, win ^ 1, wave, lane);
+      src.load(p, sm, s + 1, b ^ 1, wave, lane);
+    } else if (has_next && next.steps > 0) {
+      src.set(p, next);
+      src.load_scales(p, sm, 0, win ^ 1, wave, lane);
+      src.load(p, sm, 0, b ^ 1, wave, lane);
+    }
+    order();
+    wide_stage<KIND, OUT_BF16, MI>(p, t, s, b, win, wave, lane, sm, acc);
+    b ^= 1;
+    if ((s + 1) % kWindow == 0 || s + 1 == t.steps) win ^= 1;
+  }
+  if (t.steps == 0 && has_next && next.steps > 0) {
+    src.set(p, next);
+    step_barrier();
+    src.load_scales(p, sm, 0, win, wave, lane);
+    src.load(p, sm, 0, b, wave, lane);
+    order();
+  }
+  wide_store<OUT_BF16, MI>(p, t, KIND == kTgmm ? t.g * p.K + t.row0 : t.row0, wave, lane, acc);
+  src.t = next;
+}
+
+// Persistent workgroups, one a CU.  A group's rows are spread evenly over as few tiles as hold them; the tile range is
+// split over the XCDs, row tiles fastest, so that a group's weights are fetched once and shared in L2.
+template <Kind KIND, bool OUT_BF16>
+__global__ __launch_bounds__(kWideThreads, 2) void b128_wide_kernel(const B128Args p) {
+  __shared__ __attribute__((aligned(1024))) WideLds sm;
+  constexpr bool TG = KIND == kTgmm;
+  const int NT = static_cast<int>((p.N + kWideCols - 1) / kWideCols), RT = TG ? static_cast<int>((p.K + kWideRows - 1) / kWideRows) : 0;
+  // the group table lives in the stages while tiles are decoded, up to kDesc at a time
+  struct Table {
+    int rows_off[kMaxLocal + 1], tiles_off[kMaxLocal + 1], blocks_off[kMaxLocal + 1], tmp[kMaxLocal];
+  };
+  static_assert(sizeof(Table) <= sizeof(sm.x), "the group table fits the stages");
+  Table& gt = *reinterpret_cast<Table*>(&sm.x[0][0]);
+  int first = 0, last = 0, step = 1, n_rows = 0;
+#pragma clang loop unroll(disable)
+  for (int base = 0;; base += kDesc) {
+    const int tid = opaque(threadIdx.x);
+    __syncthreads();
+    for (int g = tid; g < p.El; g += kWideThreads) {
+      int m = p.sizes[p.g0 + g];
+      if (m < 0) {
+        if (blockIdx.x == 0) raise_error(p.err, MOE_DEVERR_GROUP_SIZE);
+        m = 0;
+      }
+      gt.tmp[g] = m;
+    }
+    __syncthreads();
+    const bool over = wave0_scan_sat(gt.tmp, gt.rows_off, p.El, p.M);
+    if (over && tid == 0 && blockIdx.x == 0) raise_error(p.err, MOE_DEVERR_ROWS);
+    __syncthreads();
+    for (int g = tid; g < p.El; g += kWideThreads) {
+      const int m = gt.rows_off[g + 1] - gt.rows_off[g];
+      gt.tmp[g] = TG ? (m + 127) / 128 : row_tiles(m, kWideRows) * NT;
+    }
+    __syncthreads();
+    wave0_scan(gt.tmp, TG ? gt.blocks_off : gt.tiles_off, p.El);
+    __syncthreads();
+    xcd_share(TG ? p.El * RT * NT : gt.tiles_off[p.El], first, last, step);
+    n_rows = gt.rows_off[p.El];
+    const int left = first < last ? (last - first + step - 1) / step - base : 0;       // this workgroup's tiles
+    const int count = min(left, kDesc);
+    if (tid < count) {
+      const int t = first + (base + tid) * step;
+      if (TG) {
+        const int g = t / (RT * NT), l = t - g * RT * NT, ct = l / RT, rt = l - ct * RT;
+        sm.desc[tid] = make_int4(kWideRows * rt, ct, g, min(kWideRows, static_cast<int>(p.K) - kWideRows * rt));
+        sm.more[tid] = make_int2(gt.blocks_off[g + 1] - gt.blocks_off[g], gt.blocks_off[g]);
+      } else {
+        const int g = find_group(gt, p.El, t);
+        const int m = gt.rows_off[g + 1] - gt.rows_off[g], nb = row_tiles(m, kWideRows), fr = tile_frags(m, nb);
+        const int local = t - gt.tiles_off[g], ct = local / nb, rt = local - ct * nb;
+        // (even filling may leave a last tile without rows: it has no steps)
+        const int rows = max(min(16 * fr, m - 16 * fr * rt), 0);
+        sm.desc[tid] = make_int4(gt.rows_off[g] + 16 * fr * rt, ct, g, rows);
+        sm.more[tid] = make_int2(rows ? static_cast<int>((p.K + 127) / 128) : 0, 0);
+      }
+    }
+    __syncthreads();
+    if (count > 0) {
+      const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+      WideSource<KIND, OUT_BF16> src;
+      src.set(p, wide_tile(sm, 0));
+      int b = 0, win = 0;
+      if (src.t.steps > 0) {
+        src.load_scales(p, sm, 0, win, wave, lane);
+        src.load(p, sm, 0, b, wave, lane);
+        order();
+      }
+#pragma clang loop unroll(disable)
+      for (int i = 0; i < count; ++i) {
+        const bool has = i + 1 < count;
+        const WideTile nt = wide_tile(sm, has ? i + 1 : i);
+        if constexpr (TG) {
+          run_wide<KIND, OUT_BF16, 8>(p, sm, src, nt, has, b, win, i > 0);
+        } else {
+          switch ((src.t.rows + 31) / 32) {
+            case 0:
+            case 1: run_wide<KIND, OUT_BF16, 1>(p, sm, src, nt, has, b, win, false); break;
+            case 2: run_wide<KIND, OUT_BF16, 2>(p, sm, src, nt, has, b, win, false); break;
+            case 3: run_wide<KIND, OUT_BF16, 3>(p, sm, src, nt, has, b, win, false); break;
+            case 4: run_wide<KIND, OUT_BF16, 4>(p, sm, src, nt, has, b, win, false); break;
+            case 5: run_wide<KIND, OUT_BF16, 5>(p, sm, src, nt, has, b, win, false); break;
+            case 6: run_wide<KIND, OUT_BF16, 6>(p, sm, src, nt, has, b, win, false); break;
+            case 7: run_wide<KIND, OUT_BF16, 7>(p, sm, src, nt, has, b, win, false); break;
+            default: run_wide<KIND, OUT_BF16, 8>(p, sm, src, nt, has, b, win, false);
+          }
+        }
+      }
+    }
+    if (left <= kDesc) break;
+  }
+  if constexpr (!TG) zero_rows<OUT_BF16, kWideThreads>(p, n_rows);
 }
 
 template <Kind KIND, bool OUT_BF16>
 hipError_t launch_b128(const B128Args& p, hipStream_t st) {
-  b128_small_kernel<KIND, OUT_BF16><<<4 * num_cus(), 64 * kSplit, 0, st>>>(p);
+  const int64_t groups = p.El < p.M ? p.El : p.M, cols = moe_cdiv(p.N, kWideCols);
+  const int64_t tiles = KIND == kTgmm ? p.El * moe_cdiv(p.K, kWideRows) * cols : (groups + p.M / kWideRows) * cols;
+  if (tiles >= num_cus())
+    b128_wide_kernel<KIND, OUT_BF16><<<num_cus(), kWideThreads, 0, st>>>(p);
+  else
+    b128_small_kernel<KIND, OUT_BF16><<<4 * num_cus(), 64 * kSplit, 0, st>>>(p);
   return hipGetLastError();
 }
 
@@ -181,7 +523,7 @@ extern "C" int moe_gmm_b128(const uint8_t* lhs, int64_t ldl, const uint8_t* lhs_
       group_offset > E - num_local_experts)
     return MOE_ERR_SHAPE;
   // row offsets inside a tile, and a group's weights' scales, are 32-bit
-  if (M > INT32_MAX - 1 || K > (1 << 22) || ldl > (1 << 23) || N > INT32_MAX || N * moe_cdiv(K, 128) > INT32_MAX) return MOE_ERR_SHAPE;
+  if (M > INT32_MAX - 1 || K > (1 << 22) || ldl > (1 << 23) || N > (1 << 22) || N * moe_cdiv(K, 128) > INT32_MAX) return MOE_ERR_SHAPE;
   // the tile table of any split of M rows into the groups stays below 2^31 entries
   if ((moe_cdiv(M, 16) + num_local_experts + 1) * (N / 16) > INT32_MAX) return MOE_ERR_SHAPE;
   if (ldl < K || ldl % 16 || lds < moe_cdiv(K, 128) || lds % 16 || lds > (1 << 23)) return MOE_ERR_SHAPE;
@@ -211,12 +553,12 @@ extern "C" int moe_tgmm_b128(const uint8_t* lhs_t, const uint8_t* lhs_scale, con
                              const int32_t* group_sizes, int32_t E, int32_t group_offset, int32_t num_local_experts, int64_t M,
                              int64_t K, int64_t N, int out_dtype, void* out, void* ws, size_t ws_bytes, void* stream) {
   using moe::tile::kMaxLocal;
-  if (M < 0 || K <= 0 || N <= 0 || K % 16 || N % 16 || K > INT32_MAX || N > INT32_MAX) return MOE_ERR_SHAPE;
+  if (M < 0 || K <= 0 || N <= 0 || K % 16 || N % 16 || K > (1 << 22) || N > (1 << 22)) return MOE_ERR_SHAPE;
   if (E <= 0 || E > 1024 || group_offset < 0 || num_local_experts < 0 || num_local_experts > kMaxLocal ||
       group_offset > E - num_local_experts)
     return MOE_ERR_SHAPE;
-  if (M > (int64_t{1} << 24) || M + 128 * static_cast<int64_t>(E) > (int64_t{1} << 24)) return MOE_ERR_SHAPE;
-  // tiles are counted in 32 bits
+  if (M > (int64_t{1} << 23) || M + 128 * static_cast<int64_t>(E) > (int64_t{1} << 23)) return MOE_ERR_SHAPE;
+  // tiles are counted in 32 bits, a tile's rows span less than 2^32 bytes
   if (moe_cdiv(K, 16) * moe_cdiv(N, 16) > INT32_MAX / (num_local_experts > 0 ? num_local_experts : 1)) return MOE_ERR_SHAPE;
   if (out_dtype == MOE_DTYPE_DEFAULT) out_dtype = MOE_F32;
   if (out_dtype != MOE_BF16 && out_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;

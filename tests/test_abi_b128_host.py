@@ -51,7 +51,7 @@ def test_quantize_weights(lib):
 def test_quantize_cols(lib):
     def f(x=AL, up=None, ldx=64, act=0, T=8, k=2, perm=AL, gs=AL, E=8, g0=0, El=8, M=16, C=64, qt=AL, st=AL, ws=AL, wsb=256):
         return lib.moe_quantize_cols_b128(x, up, ldx, act, T, k, perm, gs, E, g0, El, M, C, qt, st, ws, wsb, None)
-    check(f, [dict(C=40), dict(C=0), dict(C=BIG), dict(M=-1), dict(M=1 << 24), dict(M=(1 << 24) - 8), dict(M=BIG), dict(ldx=48), dict(ldx=68), dict(T=-1),
+    check(f, [dict(C=40), dict(C=0), dict(C=BIG), dict(M=-1), dict(M=1 << 23), dict(M=(1 << 23) - 8), dict(M=BIG), dict(ldx=48), dict(ldx=68), dict(T=-1),
               dict(T=1 << 31), dict(k=0), dict(k=65), dict(E=0), dict(E=1025), dict(g0=-1), dict(g0=4, El=5), dict(El=-1),
               dict(perm=None, T=15), dict(x=AL + 8), dict(qt=AL + 8), dict(st=AL + 8), dict(act=1, up=AL + 8)],
           [dict(act=3), dict(up=AL)], [dict(x=None), dict(gs=None), dict(qt=None), dict(st=None), dict(act=1)],
@@ -74,7 +74,7 @@ def test_gmm(lib):
 def test_tgmm(lib):
     def f(x=AL, xs=AL, y=AL, ys=AL, gs=AL, E=8, g0=0, El=8, M=16, K=144, N=32, dt=0, out=AL, ws=AL, wsb=1 << 40):
         return lib.moe_tgmm_b128(x, xs, y, ys, gs, E, g0, El, M, K, N, dt, out, ws, wsb, None)
-    check(f, [dict(K=136), dict(N=24), dict(K=0), dict(N=0), dict(K=BIG), dict(N=BIG), dict(M=-1), dict(M=1 << 24), dict(M=BIG), dict(E=0), dict(E=2000),
+    check(f, [dict(K=136), dict(N=24), dict(K=0), dict(N=0), dict(K=BIG), dict(N=BIG), dict(M=-1), dict(M=1 << 23), dict(M=BIG), dict(E=0), dict(E=2000),
               dict(g0=4, El=5), dict(x=AL + 8), dict(xs=AL + 8), dict(y=AL + 8), dict(ys=AL + 8), dict(out=AL + 8), dict(K=1 << 20, N=1 << 20)],
           [dict(dt=5), dict(dt=m.MOE_E4M3FN)], [dict(x=None), dict(xs=None), dict(y=None), dict(ys=None), dict(gs=None), dict(out=None)],
           [dict(ws=None), dict(wsb=0)], [dict(El=0, x=None, out=None)])

@@ -229,6 +229,10 @@ GMM = [  # group sizes, g0, El, K, N, spare rows
     ([0, 0], 0, 2, 128, 64, 11),
     ([1500, 300, 260, 515], 0, 4, 1152, 1536, 1),
     ([2600], 0, 1, 528, 2064, 0),
+    # as many tiles of 256 by 256 as the GPU has workgroups, and more
+    ([700, 300, 0, 616, 1200], 0, 5, 2080, 4112, 40),
+    ([9, 300, 0, 17, 1, 256, 257, 31] * 4, 1, 30, 528, 2320, 5),
+    ([513, 0, 40] * 4, 3, 7, 16, 7184, 0),
 ]
 
 
@@ -334,6 +338,8 @@ TGMM = [  # group sizes, g0, El, K, N
     ([2] * 1024, 3, 1000, 16, 32),
     ([256, 1, 513, 0, 384], 0, 5, 768, 512),
     ([2000], 0, 1, 1040, 272),
+    ([0, 2100, 1, 0, 0, 128, 129, 255, 600, 0] * 2, 0, 20, 784, 1040),
+    ([300] * 17, 0, 17, 1024, 1024),
 ]
 
 
