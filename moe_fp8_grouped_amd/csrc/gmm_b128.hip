@@ -4,8 +4,7 @@
 //   gmm    out[r, c] = sum_b sx[r, b] sw[g, b, c / 128] sum_{k in b} X[r, k] W_g[c, k]
 //   tgmm   out[g, k, c] = sum_b sx[b, k] sy[b, c] sum_{r in b} Xt[k, r] Yt[c, r]
 // One matrix instruction spans one block of the contraction, and its e8m0
-// operands apply both scales: they cost nothing.  (Float32 weight scales are
-// applied to each block's product as it is added, one operation an element.)
+// operands apply both scales: they cost nothing.
 //
 // An MFMA lane l supplies row l%16 of each operand, two 16-byte pieces of the
 // 128: elements 16*(l/16) .. and 64 + 16*(l/16) .. (any share does, as both
@@ -161,27 +160,33 @@ __global__ __launch_bounds__(64 * kSplit) void b128_small_kernel(const B128Args 
 }
 
 // ---------------------------------------------------------------- wide tiles
-// 256 x 256 results a workgroup of eight waves, two by four, each 16 MI rows by
-// 64 columns.  A stage is one block of the contraction, 128 bytes of every row
-// of both operands: whole lines, by direct loads to LDS, the next stage's
-// issued when this one's are there.  The stream runs on from tile to tile: the next
-// tile's first stage is on its way before this one's results are stored.
-constexpr int kWideThreads = 512, kWideRows = 256, kWideCols = 256, kWindow = 16, kDesc = 64;
+// Up to 320 x 256 results a workgroup of eight waves, two by four, each 16 MI rows
+// by 64 columns.  A stage is one block of the contraction, 128 bytes of every
+// row of both operands (whole lines), by direct loads to LDS, two stages of each.
+// A wave reads its weights of a stage at the stage's start; behind the barrier that
+// follows, the weights two stages on take their place, while the rows of the next
+// stage have been on their way since its start.  The stream runs on from tile to
+// tile, under the stores of the last one's results.
+constexpr int kWideThreads = 512, kWideCols = 256, kWindow = 16, kDesc = 64;
+template <Kind KIND>
+constexpr int kWideRows = KIND == kTgmm ? 256 : 320;
 
+template <Kind KIND>
 struct WideLds {
-  uint8_t x[2][kWideRows * 128];
+  uint8_t x[2][kWideRows<KIND> * 128];
   uint8_t w[2][kWideCols * 128];
-  uint8_t xs[2][kWideRows * kWindow];              // scales of a window of 16 blocks: gmm a row's 16 bytes, tgmm a block's 256
-  uint8_t ws[2][kWideCols * kWindow];              // gmm: 16 blocks by 2, a dword each
+  uint8_t xs[2][kWideRows<KIND> * kWindow];        // scales of a window of 16 blocks: gmm a row's 16 bytes, tgmm a block's 256
+  uint8_t ws[2][KIND == kTgmm ? kWideCols * kWindow : 8 * kWindow];    // gmm: 16 blocks by 2, a dword each
   int4 desc[kDesc];                                // first row, column tile, group, rows
   int2 more[kDesc];                                // blocks, first block
 };
-static_assert(sizeof(WideLds) <= 160 * 1024, "LDS of a CU");
+static_assert(sizeof(WideLds<kGmmE8M0>) <= 160 * 1024 && sizeof(WideLds<kTgmm>) <= 160 * 1024, "LDS of a CU");
 
-// Slot of 16-byte chunk c of a staged row r: c ^ swizzle(r), so that the eight rows that neighbouring lanes read lie
-// in eight slots: runs of rows, or (bf16 results) lanes l%16 at rows 8 (l%16 / 4) + l%4.
+// Slot of 16-byte chunk c of a staged row r: c ^ swizzle(r).  Rows of even and odd number lie in different halves of
+// the banks; of the sixteen rows that a read's neighbouring lanes are at, the eight of either kind lie in eight slots:
+// runs of rows, or (bf16 results) lanes l%16 at rows 8 (l%16 / 4) + l%4.
 __device__ __forceinline__ int swz_run(int r) { return (r & 7) ^ ((r >> 3) & 1); }
-__device__ __forceinline__ int swz_quads(int r) { return (r & 3) + 4 * ((r >> 3) & 1); }
+__device__ __forceinline__ int swz_quads(int r) { return ((r & 3) + 4 * ((r >> 3) & 1)) ^ ((r >> 4) & 1); }
 // First column in a wave's 64 of what lane l%16 = n supplies as weight row of fragment f: output lanes l/16 then hold
 // columns whose stores make runs of 64 bytes, eight bf16 of fragments 2 h and 2 h + 1, or four float32 of one.
 template <bool OUT_BF16>
@@ -190,16 +195,17 @@ __device__ __forceinline__ constexpr int frag_col(int f, int n) {
 }
 
 struct WideTile {
-  int64_t row0, col0;                              // (tgmm: in the group's result)
+  int row0, col0;                                  // (tgmm: in the group's result)
   int g, rows, steps, blk0;
 };
 
-__device__ __forceinline__ WideTile wide_tile(const WideLds& sm, int i) {
+template <class LDS>
+__device__ __forceinline__ WideTile wide_tile(const LDS& sm, int i) {
   const v4i d = lds_read<v4i>(lds_addr(sm.desc) + 16 * i);
   const v2i m = lds_read<v2i>(lds_addr(sm.more) + 8 * i);
   WideTile t;
   t.row0 = __builtin_amdgcn_readfirstlane(d[0]);
-  t.col0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(d[1])) * kWideCols;
+  t.col0 = __builtin_amdgcn_readfirstlane(d[1]) * kWideCols;
   t.g = __builtin_amdgcn_readfirstlane(d[2]);
   t.rows = __builtin_amdgcn_readfirstlane(d[3]);
   t.steps = __builtin_amdgcn_readfirstlane(m[0]);
@@ -207,205 +213,252 @@ __device__ __forceinline__ WideTile wide_tile(const WideLds& sm, int i) {
   return t;
 }
 
-// What the loads of a tile go by.
-template <Kind KIND, bool OUT_BF16>
-struct WideSource {
-  __amdgpu_buffer_rsrc_t x, w;
+// One operand's loads: where they are in the stream of tiles and stages, and to which buffer the next goes.
+template <Kind KIND, bool OUT_BF16, bool ROWS>
+struct Cursor {
+  __amdgpu_buffer_rsrc_t buf;
   WideTile t;
+  int i, s, b;                                     // tile, stage, buffer
+  bool more;                                       // whether there is such a stage
 
-  __device__ __forceinline__ void set(const B128Args& p, const WideTile& tile) {
-    t = tile;
-    const uint32_t cols = static_cast<uint32_t>(min(p.N - t.col0, static_cast<int64_t>(kWideCols)));
+  // The first tile from i on that has stages.
+  __device__ __forceinline__ void seek(const B128Args& p, const WideLds<KIND>& sm, int count) {
+    s = 0;
+    for (; i < count; ++i) {
+      t = wide_tile(sm, i);
+      if (t.steps > 0) break;
+    }
+    more = i < count;
+    if (!more) return;
+    const uint32_t cols = static_cast<uint32_t>(min(static_cast<int>(p.N) - t.col0, kWideCols));
     if constexpr (KIND == kTgmm) {
       const uint32_t len = 128u * t.steps, ld = static_cast<uint32_t>(p.ldx);
       const int64_t at = 128 * static_cast<int64_t>(t.blk0);
-      x = buffer(p.x + t.row0 * p.ldx + at, (t.rows - 1) * ld + len);
-      w = buffer(p.w + t.col0 * p.ldx + at, (cols - 1) * ld + len);
+      buf = ROWS ? buffer(p.x + static_cast<int64_t>(t.row0) * p.ldx + at, (t.rows - 1) * ld + len) : buffer(p.w + static_cast<int64_t>(t.col0) * p.ldx + at, (cols - 1) * ld + len);
     } else {
       const uint32_t K = static_cast<uint32_t>(p.K);
-      x = buffer(p.x + t.row0 * p.ldx, (t.rows - 1) * static_cast<uint32_t>(p.ldx) + K);
-      w = buffer(p.w + (static_cast<int64_t>(t.g) * p.N + t.col0) * p.K, cols * K);
+      buf = ROWS ? buffer(p.x + static_cast<int64_t>(t.row0) * p.ldx, (t.rows - 1) * static_cast<uint32_t>(p.ldx) + K)
+                 : buffer(p.w + (static_cast<int64_t>(t.g) * p.N + t.col0) * p.K, cols * K);
     }
   }
 
-  // Stage s to buffer b; lane l fills slot l%8 of rows 8 wave + l/8 (+ 64 i).  Rows past the tile's, columns past N and
-  // chunks past K lie outside the buffers: zeros.
-  __device__ __forceinline__ void load(const B128Args& p, WideLds& sm, int s, int b, int wave, int lane) const {
+  // The stage at hand; lane l fills slot l%8 of rows 8 wave + l/8 (+ 64 j).  Rows past the tile's, columns past N and
+  // chunks past K lie outside the buffer: zeros.  (Weights are four loads always: the waits count them.)
+  __device__ __forceinline__ void load(const B128Args& p, WideLds<KIND>& sm, int count, int wave, int lane) {
     const int r = 8 * wave + (lane >> 3);
-    const uint32_t ldx = static_cast<uint32_t>(p.ldx), ldw = KIND == kTgmm ? ldx : static_cast<uint32_t>(p.K);
-    const uint32_t xc = 16 * ((lane & 7) ^ swz_run(r)), wc = 16 * ((lane & 7) ^ (OUT_BF16 ? swz_quads(r) : swz_run(r)));
-    uint32_t xo = r * ldx + xc, wo = r * ldw + wc;
-    if (KIND != kTgmm && 128 * s + 128 > p.K) {
-      const uint32_t left = static_cast<uint32_t>(p.K) - 128u * s;
-      xo = xc < left ? xo : 0x80000000u;
-      wo = wc < left ? wo : 0x80000000u;
-    }
+    const uint32_t ld = static_cast<uint32_t>(ROWS || KIND == kTgmm ? p.ldx : p.K);
+    const uint32_t c = 16 * ((lane & 7) ^ (ROWS || !OUT_BF16 ? swz_run(r) : swz_quads(r)));
+    uint32_t off = r * ld + c;
+    if (KIND != kTgmm && 128 * s + 128 > p.K) off = c < static_cast<uint32_t>(p.K) - 128u * s ? off : 0x80000000u;
+    uint8_t* dst = (ROWS ? sm.x[b] : sm.w[b]) + 8 * wave * 128;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(w, (lds_void*)(sm.w[b] + (64 * i + 8 * wave) * 128), 16, wo, 128u * s + 64 * i * ldw, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (64 * i + 8 * wave < t.rows)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(x, (lds_void*)(sm.x[b] + (64 * i + 8 * wave) * 128), 16, xo, 128u * s + 64 * i * ldx, 0, 0);
-  }
-
-  // Scales of blocks 16 win .. to buffer b.  (Lanes past the tile or the contraction fetch what is there of its last.)
-  __device__ __forceinline__ void load_scales(const B128Args& p, WideLds& sm, int win, int b, int wave, int lane) const {
-    if constexpr (KIND == kTgmm) {                 // [block][K or N]: lanes 16 j .. 16 j + 15 the 256 bytes of block 4 wave + j
-      const int blk = kWindow * win + 4 * (wave & 3) + (lane >> 4);
-      const int64_t n = wave < 4 ? p.K : p.N, c = (wave < 4 ? t.row0 : t.col0) + 16 * (lane & 15);
-      const uint8_t* src = (wave < 4 ? p.xs : static_cast<const uint8_t*>(p.ws)) +
-                           (t.blk0 + min(blk, t.steps - 1)) * n + min(c, n - 16);
-      uint8_t* dst = (wave < 4 ? sm.xs[b] : sm.ws[b]) + 1024 * (wave & 3);
-      __builtin_amdgcn_global_load_lds(src, (lds_void*)dst, 16, 0, 0);
-    } else {
-      if (lane < 32 && 32 * wave < t.rows) {
-        const int64_t row = t.row0 + min(32 * wave + lane, t.rows - 1);
-        __builtin_amdgcn_global_load_lds(p.xs + row * p.lds + kWindow * win, (lds_void*)(sm.xs[b] + 512 * wave), 16, 0, 0);
-      }
-      if (wave == 7 && lane < 32) {                // block win * 16 + lane / 2, column block lane & 1 of the tile's two
-        const int64_t nb = (p.N + 127) / 128;
-        const int64_t c = min(t.col0 / 128 + (lane & 1), nb - 1);
-        const int64_t at = (static_cast<int64_t>(t.g) * t.steps + min(kWindow * win + (lane >> 1), t.steps - 1)) * nb + c;
-        const uint8_t* src = static_cast<const uint8_t*>(p.ws) + (KIND == kGmmF32 ? 4 * at : at);
-        if (KIND == kGmmE8M0) src -= reinterpret_cast<uintptr_t>(src) & 3;         // the dword that holds the byte
-        __builtin_amdgcn_global_load_lds(src, (lds_void*)sm.ws[b], 4, 0, 0);
-      }
+    for (int j = 0; j < (ROWS ? kWideRows<KIND> : kWideCols) / 64; ++j)
+      if (!ROWS || 64 * j + 8 * wave < t.rows)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void*)(dst + 64 * 128 * j), 16, off, 128u * s + 64 * j * ld, 0, 0);
+    b ^= 1;
+    if (++s == t.steps) {
+      ++i;
+      seek(p, sm, count);
     }
   }
 };
 
-template <Kind KIND, bool OUT_BF16, int MI>
-__device__ __forceinline__ void wide_stage(const B128Args& p, const WideTile& t, int s, int b, int win, int wave, int lane,
-                                           const WideLds& sm, v4f (&acc)[MI][4]) {
-  const int l15 = lane & 15, grp = lane >> 4, wr = wave >> 2, wc = wave & 3;
-  const int xr = 16 * MI * wr + l15, wrow = 64 * wc + frag_col<OUT_BF16>(0, l15);
-  const uint32_t xa = lds_addr(sm.x[0]) + b * static_cast<uint32_t>(sizeof(sm.x[0])) + xr * 128 + 16 * (grp ^ swz_run(l15));
-  const uint32_t wa = lds_addr(sm.w[0]) + b * static_cast<uint32_t>(sizeof(sm.w[0])) + wrow * 128 +
-                      16 * (grp ^ (OUT_BF16 ? swz_quads(wrow) : swz_run(wrow)));
-  const uint32_t xsb = lds_addr(sm.xs[0]) + win * static_cast<uint32_t>(sizeof(sm.xs[0]));
-  const uint32_t wsb = lds_addr(sm.ws[0]) + win * static_cast<uint32_t>(sizeof(sm.ws[0]));
-  const int sb = s & (kWindow - 1);
-  v8i w[4];
-  uint32_t wsc[4];
-  float wf = 0.0f;
-#pragma unroll
-  for (int f = 0; f < 4; ++f) {
-    const uint32_t at = frag_col<OUT_BF16>(f, 0) * 128;
-    w[f] = frag(__builtin_bit_cast(uint4, lds_read<v4i>(wa + at)), __builtin_bit_cast(uint4, lds_read<v4i>((wa ^ 64u) + at)));
-    if (KIND == kTgmm) wsc[f] = lds_read<uint8_t>(wsb + 256 * sb + wrow + frag_col<OUT_BF16>(f, 0));
-  }
-  if constexpr (KIND == kGmmE8M0) {
-    const int64_t nb = (p.N + 127) / 128, c = min(t.col0 / 128 + (wc >> 1), nb - 1);
-    const int64_t at = (static_cast<int64_t>(t.g) * t.steps + s) * nb + c;
-    const uint32_t byte = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.ws) + at) & 3;
-    wsc[0] = wsc[1] = wsc[2] = wsc[3] = lds_read<uint8_t>(wsb + 8 * sb + 4 * (wc >> 1) + byte);
-  }
-  if constexpr (KIND == kGmmF32) wf = lds_read<float>(wsb + 8 * sb + 4 * (wc >> 1));
-#pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const v8i x = frag(__builtin_bit_cast(uint4, lds_read<v4i>(xa + 2048 * i)), __builtin_bit_cast(uint4, lds_read<v4i>((xa ^ 64u) + 2048 * i)));
-    const uint32_t xs = KIND == kTgmm ? lds_read<uint8_t>(xsb + 256 * sb + xr + 16 * i) : lds_read<uint8_t>(xsb + (xr + 16 * i) * kWindow + sb);
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      if constexpr (KIND == kGmmF32)
-        acc[i][f] += wf * mfma_scaled(w[f], 127, x, xs, v4f{0.f, 0.f, 0.f, 0.f});
-      else
-        acc[i][f] = mfma_scaled(w[f], wsc[f], x, xs, acc[i][f]);
+// Scales of blocks 16 n .. of tile t to window buffer `win`.  (Lanes past the tile or the contraction fetch what is there
+// of its last.)
+template <Kind KIND>
+__device__ __forceinline__ void load_scales(const B128Args& p, WideLds<KIND>& sm, const WideTile& t, int n, int win, int wave, int lane) {
+  if constexpr (KIND == kTgmm) {                   // [block][K or N]: lanes 16 j .. 16 j + 15 the 256 bytes of block 4 wave + j
+    const int blk = kWindow * n + 4 * (wave & 3) + (lane >> 4);
+    const int64_t len = wave < 4 ? p.K : p.N, c = (wave < 4 ? t.row0 : t.col0) + 16 * (lane & 15);
+    const uint8_t* src = (wave < 4 ? p.xs : static_cast<const uint8_t*>(p.ws)) + (t.blk0 + min(blk, t.steps - 1)) * len + min(c, len - 16);
+    uint8_t* dst = (wave < 4 ? sm.xs[win] : sm.ws[win]) + 1024 * (wave & 3);
+    __builtin_amdgcn_global_load_lds(src, (lds_void*)dst, 16, 0, 0);
+  } else {
+    constexpr int R = kWideRows<KIND> / 8;
+    if (lane < R && R * wave < t.rows) {
+      const int64_t row = t.row0 + min(R * wave + lane, t.rows - 1);
+      __builtin_amdgcn_global_load_lds(p.xs + row * p.lds + kWindow * n, (lds_void*)(sm.xs[win] + R * kWindow * wave), 16, 0, 0);
+    }
+    if (wave == 7 && lane < 2 * kWindow) {         // block 16 n + lane / 2, column block lane & 1 of the tile's two
+      const int nb = static_cast<int>((p.N + 127) / 128), c = min(t.col0 / 128 + (lane & 1), nb - 1);
+      const int64_t at = (static_cast<int64_t>(t.g) * t.steps + min(kWindow * n + (lane >> 1), t.steps - 1)) * nb + c;
+      const uint8_t* src = static_cast<const uint8_t*>(p.ws) + (KIND == kGmmF32 ? 4 * at : at);
+      if (KIND == kGmmE8M0) src -= reinterpret_cast<uintptr_t>(src) & 3;           // the dword that holds the byte
+      __builtin_amdgcn_global_load_lds(src, (lds_void*)sm.ws[win], 4, 0, 0);
     }
   }
 }
 
 // Every store is issued whatever the tile holds (rows past it, columns past N lie outside the buffer), so that their
 // number is known to the waits.
-template <bool OUT_BF16, int MI>
-__device__ __forceinline__ void wide_store(const B128Args& p, const WideTile& t, int64_t out_row0, int wave, int lane, const v4f (&acc)[MI][4]) {
+template <Kind KIND, bool OUT_BF16, int MI>
+__device__ __forceinline__ void wide_store(const B128Args& p, const WideTile& t, int wave, int lane, const v4f (&acc)[MI][4], float scale) {
   constexpr int B = OUT_BF16 ? 2 : 4;
   const int l15 = lane & 15, grp = lane >> 4, wr = wave >> 2, wc = wave & 3;
   const uint32_t ld = static_cast<uint32_t>(p.N) * B;
-  const int64_t c = t.col0 + 64 * wc;
-  uint8_t* base = static_cast<uint8_t*>(p.out) + (out_row0 + 16 * MI * wr) * p.N * B + c * B;
+  const int64_t c = t.col0 + 64 * wc, row0 = (KIND == kTgmm ? t.g * p.K + t.row0 : t.row0) + 16 * MI * wr;
   const int rows = t.rows - 16 * MI * wr;          // the wave's rows (or none)
   const int64_t left = p.N - c;                    // its columns
-  const __amdgpu_buffer_rsrc_t o = buffer(base, rows > 0 && left > 0 ? (rows - 1) * ld + static_cast<uint32_t>(min(left, static_cast<int64_t>(64))) * B : 0u);
+  const __amdgpu_buffer_rsrc_t o = buffer(static_cast<uint8_t*>(p.out) + (row0 * p.N + c) * B,
+                                          rows > 0 && left > 0 ? (rows - 1) * ld + static_cast<uint32_t>(min(left, static_cast<int64_t>(64))) * B : 0u);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const uint32_t row = (16 * i + l15) * ld;
+    v4f v[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) v[f] = KIND == kGmmF32 ? acc[i][f] * scale : acc[i][f];
     if (OUT_BF16) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        v4u32 v;
+        v4u32 u;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const v4f& a = acc[i][2 * h + (q >> 1)];
-          v[q] = f32_to_bf16(a[2 * (q & 1)]) | static_cast<uint32_t>(f32_to_bf16(a[2 * (q & 1) + 1])) << 16;
+          const v4f& a = v[2 * h + (q >> 1)];
+          u[q] = f32_to_bf16(a[2 * (q & 1)]) | static_cast<uint32_t>(f32_to_bf16(a[2 * (q & 1) + 1])) << 16;
         }
         const int col = 32 * h + 8 * grp;
-        __builtin_amdgcn_raw_buffer_store_b128(v, o, col < left ? row + 2 * col : 0xf0000000u, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(u, o, col < left ? row + 2 * col : 0xf0000000u, 0, 0);
       }
     } else {
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
         const int col = 16 * f + 4 * grp;
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, acc[i][f]), o, col < left ? row + 4 * col : 0xf0000000u, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, v[f]), o, col < left ? row + 4 * col : 0xf0000000u, 0, 0);
       }
     }
   }
 }
 
-// One tile from the stream: `src` holds it, its first stage is loaded (or on its way) in buffer b; `next` (if there is one)
-// the tile that follows.  `behind`: its first stage was issued before the last tile's stores.
+// Where a workgroup is in its tiles.
+template <Kind KIND, bool OUT_BF16>
+struct Stream {
+  Cursor<KIND, OUT_BF16, true> x;
+  Cursor<KIND, OUT_BF16, false> w;
+  int count;
+  int b, win;                                      // buffers of the stage at hand
+  bool ahead;                                      // whether weights were issued behind the rows that are waited for
+
+  // The next rows, and with a window's first its scales (to the window that is not in use).
+  __device__ __forceinline__ void load_rows(const B128Args& p, WideLds<KIND>& sm, int to, int wave, int lane) {
+    if (!x.more) return;
+    if (x.s % kWindow == 0) load_scales<KIND>(p, sm, x.t, x.s / kWindow, to, wave, lane);
+    x.load(p, sm, count, wave, lane);
+  }
+};
+
+// One tile.
 template <Kind KIND, bool OUT_BF16, int MI>
-__device__ __forceinline__ void run_wide(const B128Args& p, WideLds& sm, WideSource<KIND, OUT_BF16>& src, const WideTile& next,
-                                         bool has_next, int& b, int& win, bool behind) {
+__device__ __forceinline__ void run_wide(const B128Args& p, WideLds<KIND>& sm, Stream<KIND, OUT_BF16>& st, const WideTile& t, bool stored) {
   constexpr int kStores = (OUT_BF16 ? 2 : 4) * MI;
   const int tid = opaque(threadIdx.x);
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const WideTile t = src.t;
+  const int l15 = lane & 15, grp = lane >> 4, wr = wave >> 2, wc = wave & 3;
+  const int xr = 16 * MI * wr + l15, wrow = 64 * wc + frag_col<OUT_BF16>(0, l15);
+  const uint32_t xa0 = lds_addr(sm.x[0]) + xr * 128 + 16 * (grp ^ swz_run(l15));
+  const uint32_t wa0 = lds_addr(sm.w[0]) + wrow * 128 + 16 * (grp ^ (OUT_BF16 ? swz_quads(wrow) : swz_run(wrow)));
   v4f acc[MI][4];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int f = 0; f < 4; ++f) acc[i][f] = v4f{0.f, 0.f, 0.f, 0.f};
+  uint32_t xsd[MI];                                // gmm: a dword of each row's scales, four blocks
+  float unit = 1.0f;                               // float32 scales: what the sums are in units of
 #pragma clang loop unroll(disable)
   for (int s = 0; s < t.steps; ++s) {
-    if (KIND == kTgmm && s == 0 && behind)
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm(kStores));       // this wave's loads of stage s are there, the stores may be on their way
-    else
+    // this wave's loads of the stage are there: the weights of the next may be on their way, and a tile's stores
+    if (!st.ahead)
       __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-    step_barrier();                                          // every wave's are; the other buffer is read
+    else if (KIND == kTgmm && s == 0 && stored)
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(4 + kStores));
+    else
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(4));
+    step_barrier();                                // every wave's are; the other buffer of rows is read
+    const bool last_of_window = (s + 1) % kWindow == 0 || s + 1 == t.steps;
+    st.load_rows(p, sm, st.win ^ 1, wave, lane);
     order();
-    if (s + 1 < t.steps) {
-      if ((s + 1) % kWindow == 0) src.load_scales(p, sm, (s + 1) / kWindow, win ^ 1, wave, lane);
-      src.load(p, sm, s + 1, b ^ 1, wave, lane);
-    } else if (has_next && next.steps > 0) {
-      src.set(p, next);
-      src.load_scales(p, sm, 0, win ^ 1, wave, lane);
-      src.load(p, sm, 0, b ^ 1, wave, lane);
+    const uint32_t xa = xa0 + st.b * static_cast<uint32_t>(sizeof(sm.x[0])), wa = wa0 + st.b * static_cast<uint32_t>(sizeof(sm.w[0]));
+    const uint32_t xsb = lds_addr(sm.xs[0]) + st.win * static_cast<uint32_t>(sizeof(sm.xs[0]));
+    const uint32_t wsb = lds_addr(sm.ws[0]) + st.win * static_cast<uint32_t>(sizeof(sm.ws[0]));
+    const int sb = s & (kWindow - 1);
+    auto read_x = [&](int i) {
+      return frag(__builtin_bit_cast(uint4, lds_read<v4i>(xa + 2048 * i)), __builtin_bit_cast(uint4, lds_read<v4i>((xa ^ 64u) + 2048 * i)));
+    };
+    v8i w[4];
+    uint32_t wsc[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const uint32_t at = frag_col<OUT_BF16>(f, 0) * 128;
+      w[f] = frag(__builtin_bit_cast(uint4, lds_read<v4i>(wa + at)), __builtin_bit_cast(uint4, lds_read<v4i>((wa ^ 64u) + at)));
+      if (KIND == kTgmm) wsc[f] = lds_read<uint8_t>(wsb + 256 * sb + wrow + frag_col<OUT_BF16>(f, 0));
+    }
+    v8i x[2];
+    x[0] = read_x(0);
+    if constexpr (KIND == kTgmm) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) xsd[i] = lds_read<uint8_t>(xsb + 256 * sb + xr + 16 * i);
+    } else if ((sb & 3) == 0) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) xsd[i] = lds_read<uint32_t>(xsb + (xr + 16 * i) * kWindow + sb);
+    }
+    float ratio = 1.0f;
+    if constexpr (KIND == kGmmE8M0) {
+      const uint32_t nb = static_cast<uint32_t>((p.N + 127) / 128), c = min(static_cast<uint32_t>(t.col0) / 128 + (wc >> 1), nb - 1);
+      const uint32_t byte = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.ws)) + (static_cast<uint32_t>(t.g) * t.steps + s) * nb + c) & 3;
+      wsc[0] = wsc[1] = wsc[2] = wsc[3] = lds_read<uint8_t>(wsb + 8 * sb + 4 * (wc >> 1) + byte);
+    }
+    if constexpr (KIND == kGmmF32) {
+      // The scale is a power of two, which the matrix core applies, times a factor in [1, 2) (or below, for a subnormal):
+      // the sums are held in units of the last block's factor, and change units by the ratio of two.
+      const uint32_t v = __builtin_amdgcn_readfirstlane(lds_read<uint32_t>(wsb + 8 * sb + 4 * (wc >> 1)));
+      const uint32_t e = (v >> 23) & 255u;
+      float m = __uint_as_float((v & 0x807fffffu) | 0x3f800000u);
+      if (e == 0u) m = __uint_as_float(v) * 0x1p127f;
+      if (e == 255u) m = 1.0f;                     // (its results are NaN)
+      if (m == 0.0f) {                             // a block of scale 0: no sum changes
+        m = unit;
+#pragma unroll
+        for (int f = 0; f < 4; ++f) w[f] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
+      }
+      if (s > 0) ratio = unit / m;
+      unit = m;
+      wsc[0] = wsc[1] = wsc[2] = wsc[3] = e;
+    }
+    step_barrier();                                // every wave's weights are read
+    if (st.w.more) {
+      st.w.load(p, sm, st.count, wave, lane);
+      st.ahead = true;
+    } else {
+      st.ahead = false;
     }
     order();
-    wide_stage<KIND, OUT_BF16, MI>(p, t, s, b, win, wave, lane, sm, acc);
-    b ^= 1;
-    if ((s + 1) % kWindow == 0 || s + 1 == t.steps) win ^= 1;
+    const uint32_t shift = KIND == kTgmm ? 0 : 8 * (sb & 3);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      if (i + 1 < MI) x[(i + 1) & 1] = read_x(i + 1);
+      __builtin_amdgcn_sched_barrier(0);           // (left free, the compiler reads each block's rows behind the last one's products)
+      const uint32_t xs = xsd[i] >> shift;
+      if constexpr (KIND == kGmmF32) {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) acc[i][f] *= ratio;
+      }
+#pragma unroll
+      for (int f = 0; f < 4; ++f) acc[i][f] = mfma_scaled(w[f], wsc[f], x[i & 1], xs, acc[i][f]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    st.b ^= 1;
+    if (last_of_window) st.win ^= 1;
   }
-  if (t.steps == 0 && has_next && next.steps > 0) {
-    src.set(p, next);
-    step_barrier();
-    src.load_scales(p, sm, 0, win, wave, lane);
-    src.load(p, sm, 0, b, wave, lane);
-    order();
-  }
-  wide_store<OUT_BF16, MI>(p, t, KIND == kTgmm ? t.g * p.K + t.row0 : t.row0, wave, lane, acc);
-  src.t = next;
+  wide_store<KIND, OUT_BF16, MI>(p, t, wave, lane, acc, unit);
 }
 
 // Persistent workgroups, one a CU.  A group's rows are spread evenly over as few tiles as hold them; the tile range is
 // split over the XCDs, row tiles fastest, so that a group's weights are fetched once and shared in L2.
 template <Kind KIND, bool OUT_BF16>
 __global__ __launch_bounds__(kWideThreads, 2) void b128_wide_kernel(const B128Args p) {
-  __shared__ __attribute__((aligned(1024))) WideLds sm;
+  __shared__ __attribute__((aligned(1024))) WideLds<KIND> sm;
   constexpr bool TG = KIND == kTgmm;
-  const int NT = static_cast<int>((p.N + kWideCols - 1) / kWideCols), RT = TG ? static_cast<int>((p.K + kWideRows - 1) / kWideRows) : 0;
+  constexpr int ROWS = kWideRows<KIND>;
+  const int NT = static_cast<int>((p.N + kWideCols - 1) / kWideCols), RT = TG ? static_cast<int>((p.K + ROWS - 1) / ROWS) : 0;
   // the group table lives in the stages while tiles are decoded, up to kDesc at a time
   struct Table {
     int rows_off[kMaxLocal + 1], tiles_off[kMaxLocal + 1], blocks_off[kMaxLocal + 1], tmp[kMaxLocal];
@@ -431,7 +484,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_wide_kernel(const B128Ar
     __syncthreads();
     for (int g = tid; g < p.El; g += kWideThreads) {
       const int m = gt.rows_off[g + 1] - gt.rows_off[g];
-      gt.tmp[g] = TG ? (m + 127) / 128 : row_tiles(m, kWideRows) * NT;
+      gt.tmp[g] = TG ? (m + 127) / 128 : row_tiles(m, ROWS) * NT;
     }
     __syncthreads();
     wave0_scan(gt.tmp, TG ? gt.blocks_off : gt.tiles_off, p.El);
@@ -444,13 +497,13 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_wide_kernel(const B128Ar
       const int t = first + (base + tid) * step;
       if (TG) {
         const int g = t / (RT * NT), l = t - g * RT * NT, ct = l / RT, rt = l - ct * RT;
-        sm.desc[tid] = make_int4(kWideRows * rt, ct, g, min(kWideRows, static_cast<int>(p.K) - kWideRows * rt));
+        sm.desc[tid] = make_int4(ROWS * rt, ct, g, min(ROWS, static_cast<int>(p.K) - ROWS * rt));
         sm.more[tid] = make_int2(gt.blocks_off[g + 1] - gt.blocks_off[g], gt.blocks_off[g]);
       } else {
         const int g = find_group(gt, p.El, t);
-        const int m = gt.rows_off[g + 1] - gt.rows_off[g], nb = row_tiles(m, kWideRows), fr = tile_frags(m, nb);
+        const int m = gt.rows_off[g + 1] - gt.rows_off[g], nb = row_tiles(m, ROWS), fr = tile_frags(m, nb);
         const int local = t - gt.tiles_off[g], ct = local / nb, rt = local - ct * nb;
-        // (even filling may leave a last tile without rows: it has no steps)
+        // (even filling may leave a last tile without rows: it has no stages)
         const int rows = max(min(16 * fr, m - 16 * fr * rt), 0);
         sm.desc[tid] = make_int4(gt.rows_off[g] + 16 * fr * rt, ct, g, rows);
         sm.more[tid] = make_int2(rows ? static_cast<int>((p.K + 127) / 128) : 0, 0);
@@ -459,31 +512,37 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_wide_kernel(const B128Ar
     __syncthreads();
     if (count > 0) {
       const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-      WideSource<KIND, OUT_BF16> src;
-      src.set(p, wide_tile(sm, 0));
-      int b = 0, win = 0;
-      if (src.t.steps > 0) {
-        src.load_scales(p, sm, 0, win, wave, lane);
-        src.load(p, sm, 0, b, wave, lane);
-        order();
-      }
+      Stream<KIND, OUT_BF16> st;
+      st.count = count;
+      st.b = st.win = 0;
+      st.x.i = st.x.b = st.w.i = st.w.b = 0;
+      st.x.seek(p, sm, count);
+      st.w.seek(p, sm, count);
+      if (st.w.more) st.w.load(p, sm, count, wave, lane);
+      order();
+      st.load_rows(p, sm, 0, wave, lane);
+      order();
+      st.ahead = st.w.more;
+      if (st.w.more) st.w.load(p, sm, count, wave, lane);
+      order();
 #pragma clang loop unroll(disable)
       for (int i = 0; i < count; ++i) {
-        const bool has = i + 1 < count;
-        const WideTile nt = wide_tile(sm, has ? i + 1 : i);
+        const WideTile t = wide_tile(sm, i);
         if constexpr (TG) {
-          run_wide<KIND, OUT_BF16, 8>(p, sm, src, nt, has, b, win, i > 0);
+          run_wide<KIND, OUT_BF16, 8>(p, sm, st, t, i > 0);
         } else {
-          switch ((src.t.rows + 31) / 32) {
-            case 0:
-            case 1: run_wide<KIND, OUT_BF16, 1>(p, sm, src, nt, has, b, win, false); break;
-            case 2: run_wide<KIND, OUT_BF16, 2>(p, sm, src, nt, has, b, win, false); break;
-            case 3: run_wide<KIND, OUT_BF16, 3>(p, sm, src, nt, has, b, win, false); break;
-            case 4: run_wide<KIND, OUT_BF16, 4>(p, sm, src, nt, has, b, win, false); break;
-            case 5: run_wide<KIND, OUT_BF16, 5>(p, sm, src, nt, has, b, win, false); break;
-            case 6: run_wide<KIND, OUT_BF16, 6>(p, sm, src, nt, has, b, win, false); break;
-            case 7: run_wide<KIND, OUT_BF16, 7>(p, sm, src, nt, has, b, win, false); break;
-            default: run_wide<KIND, OUT_BF16, 8>(p, sm, src, nt, has, b, win, false);
+          switch ((t.rows + 31) / 32) {
+            case 0: break;
+            case 1: run_wide<KIND, OUT_BF16, 1>(p, sm, st, t, false); break;
+            case 2: run_wide<KIND, OUT_BF16, 2>(p, sm, st, t, false); break;
+            case 3: run_wide<KIND, OUT_BF16, 3>(p, sm, st, t, false); break;
+            case 4: run_wide<KIND, OUT_BF16, 4>(p, sm, st, t, false); break;
+            case 5: run_wide<KIND, OUT_BF16, 5>(p, sm, st, t, false); break;
+            case 6: run_wide<KIND, OUT_BF16, 6>(p, sm, st, t, false); break;
+            case 7: run_wide<KIND, OUT_BF16, 7>(p, sm, st, t, false); break;
+            case 8: run_wide<KIND, OUT_BF16, 8>(p, sm, st, t, false); break;
+            case 9: run_wide<KIND, OUT_BF16, 9>(p, sm, st, t, false); break;
+            default: run_wide<KIND, OUT_BF16, 10>(p, sm, st, t, false);
           }
         }
       }
@@ -496,7 +555,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_wide_kernel(const B128Ar
 template <Kind KIND, bool OUT_BF16>
 hipError_t launch_b128(const B128Args& p, hipStream_t st) {
   const int64_t groups = p.El < p.M ? p.El : p.M, cols = moe_cdiv(p.N, kWideCols);
-  const int64_t tiles = KIND == kTgmm ? p.El * moe_cdiv(p.K, kWideRows) * cols : (groups + p.M / kWideRows) * cols;
+  const int64_t tiles = KIND == kTgmm ? p.El * moe_cdiv(p.K, kWideRows<KIND>) * cols : (groups + p.M / kWideRows<KIND>) * cols;
   if (tiles >= num_cus())
     b128_wide_kernel<KIND, OUT_BF16><<<num_cus(), kWideThreads, 0, st>>>(p);
   else
