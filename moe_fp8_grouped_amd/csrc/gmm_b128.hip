@@ -11,6 +11,8 @@
 // operands take the same and the scale is one for all).  The product is formed
 // transposed per 16 x 16 block (the weights are the first operand), so output
 // lane l holds row l%16 and four consecutive columns 4*(l/16) .. +3.
+#include <type_traits>
+
 #include "b128_common.hpp"
 #include "stage_common.hpp"
 
@@ -35,8 +37,10 @@ struct B128Args {
   int32_t* err;
 };
 
+// The scale operands' bytes: the lowest of ws, byte XB of xs.
+template <int XB = 0>
 __device__ __forceinline__ v4f mfma_scaled(const v8i& w, uint32_t ws, const v8i& x, uint32_t xs, const v4f& c) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 0, 0, 0, ws, 0, xs);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 0, 0, 0, ws, XB, xs);
 }
 
 __device__ __forceinline__ v8i frag(const uint4& a, const uint4& b) {
@@ -44,12 +48,18 @@ __device__ __forceinline__ v8i frag(const uint4& a, const uint4& b) {
              static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w)};
 }
 
+// Two values to bfloat16, nearest even, in one operation (f32_to_bf16 takes eight for each).
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, v2bf));
+}
+
 template <bool OUT_BF16>
 __device__ __forceinline__ void store4(void* out, int64_t at, const v4f& v) {
   if (OUT_BF16)
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
-        make_uint2(f32_to_bf16(v[0]) | static_cast<uint32_t>(f32_to_bf16(v[1])) << 16,
-                   f32_to_bf16(v[2]) | static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
+        make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
   else
     *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(v[0], v[1], v[2], v[3]);
 }
@@ -194,6 +204,13 @@ __device__ __forceinline__ constexpr int frag_col(int f, int n) {
   return OUT_BF16 ? 32 * (f >> 1) + 8 * (n >> 2) + 4 * (f & 1) + (n & 3) : 16 * f + n;
 }
 
+// Row of the tile at staged place r.  gmm: r.  tgmm: of a wave's 128 places, 16 i + n holds row 8 n + i, so that the scales
+// of the eight rows that lane n multiplies are neighbours.
+template <Kind KIND>
+__device__ __forceinline__ int row_at(int r) {
+  return KIND == kTgmm ? (r & ~127) + 8 * (r & 15) + ((r >> 4) & 7) : r;
+}
+
 struct WideTile {
   int row0, col0;                                  // (tgmm: in the group's result)
   int g, rows, steps, blk0;
@@ -248,13 +265,14 @@ struct Cursor {
     const int r = 8 * wave + (lane >> 3);
     const uint32_t ld = static_cast<uint32_t>(ROWS || KIND == kTgmm ? p.ldx : p.K);
     const uint32_t c = 16 * ((lane & 7) ^ (ROWS || !OUT_BF16 ? swz_run(r) : swz_quads(r)));
-    uint32_t off = r * ld + c;
+    // (64 places further on: tgmm 4 rows, and then the wave's other 128)
+    uint32_t off = (ROWS ? row_at<KIND>(r) : r) * ld + c;
     if (KIND != kTgmm && 128 * s + 128 > p.K) off = c < static_cast<uint32_t>(p.K) - 128u * s ? off : 0x80000000u;
     uint8_t* dst = (ROWS ? sm.x[b] : sm.w[b]) + 8 * wave * 128;
 #pragma unroll
     for (int j = 0; j < (ROWS ? kWideRows<KIND> : kWideCols) / 64; ++j)
-      if (!ROWS || 64 * j + 8 * wave < t.rows)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void*)(dst + 64 * 128 * j), 16, off, 128u * s + 64 * j * ld, 0, 0);
+      if (!ROWS || KIND == kTgmm || 64 * j + 8 * wave < t.rows)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void*)(dst + 64 * 128 * j), 16, off, 128u * s + (ROWS ? row_at<KIND>(64 * j) : 64 * j) * ld, 0, 0);
     b ^= 1;
     if (++s == t.steps) {
       ++i;
@@ -263,28 +281,32 @@ struct Cursor {
   }
 };
 
-// Scales of blocks 16 n .. of tile t to window buffer `win`.  (Lanes past the tile or the contraction fetch what is there
-// of its last.)
+// Scales of blocks 16 n .. of tile t to window buffer `win`.  (What lies past the tile or the contraction is some scale or
+// zero, and not used.  Buffer loads, as for the stages: behind a global load to LDS the compiler takes LDS reads to
+// come back in any order, and waits for all of them at each use.)
 template <Kind KIND>
 __device__ __forceinline__ void load_scales(const B128Args& p, WideLds<KIND>& sm, const WideTile& t, int n, int win, int wave, int lane) {
   if constexpr (KIND == kTgmm) {                   // [block][K or N]: lanes 16 j .. 16 j + 15 the 256 bytes of block 4 wave + j
-    const int blk = kWindow * n + 4 * (wave & 3) + (lane >> 4);
-    const int64_t len = wave < 4 ? p.K : p.N, c = (wave < 4 ? t.row0 : t.col0) + 16 * (lane & 15);
-    const uint8_t* src = (wave < 4 ? p.xs : static_cast<const uint8_t*>(p.ws)) + (t.blk0 + min(blk, t.steps - 1)) * len + min(c, len - 16);
-    uint8_t* dst = (wave < 4 ? sm.xs[win] : sm.ws[win]) + 1024 * (wave & 3);
-    __builtin_amdgcn_global_load_lds(src, (lds_void*)dst, 16, 0, 0);
+    const bool x = wave < 4;
+    const int64_t len = x ? p.K : p.N, c = x ? t.row0 : t.col0;
+    const uint8_t* src = (x ? p.xs : static_cast<const uint8_t*>(p.ws)) + (t.blk0 + static_cast<int64_t>(kWindow) * n) * len + c;
+    const __amdgpu_buffer_rsrc_t buf = buffer(src, static_cast<uint32_t>(min(t.steps - kWindow * n, kWindow) * len - c));
+    uint8_t* dst = (x ? sm.xs[win] : sm.ws[win]) + 1024 * (wave & 3);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void*)dst, 16, (4 * (wave & 3) + (lane >> 4)) * static_cast<uint32_t>(len) + 16 * (lane & 15), 0, 0, 0);
   } else {
     constexpr int R = kWideRows<KIND> / 8;
     if (lane < R && R * wave < t.rows) {
-      const int64_t row = t.row0 + min(R * wave + lane, t.rows - 1);
-      __builtin_amdgcn_global_load_lds(p.xs + row * p.lds + kWindow * n, (lds_void*)(sm.xs[win] + R * kWindow * wave), 16, 0, 0);
+      const uint32_t lds = static_cast<uint32_t>(p.lds);
+      const __amdgpu_buffer_rsrc_t buf = buffer(p.xs + t.row0 * p.lds, t.rows * lds);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void*)(sm.xs[win] + R * kWindow * wave), 16, (R * wave + lane) * lds, kWindow * n, 0, 0);
     }
     if (wave == 7 && lane < 2 * kWindow) {         // block 16 n + lane / 2, column block lane & 1 of the tile's two
-      const int nb = static_cast<int>((p.N + 127) / 128), c = min(t.col0 / 128 + (lane & 1), nb - 1);
-      const int64_t at = (static_cast<int64_t>(t.g) * t.steps + min(kWindow * n + (lane >> 1), t.steps - 1)) * nb + c;
-      const uint8_t* src = static_cast<const uint8_t*>(p.ws) + (KIND == kGmmF32 ? 4 * at : at);
-      if (KIND == kGmmE8M0) src -= reinterpret_cast<uintptr_t>(src) & 3;           // the dword that holds the byte
-      __builtin_amdgcn_global_load_lds(src, (lds_void*)sm.ws[win], 4, 0, 0);
+      const int nb = static_cast<int>((p.N + 127) / 128), size = KIND == kGmmF32 ? 4 : 1;
+      const uint8_t* src = static_cast<const uint8_t*>(p.ws) + static_cast<int64_t>(t.g) * t.steps * nb * size;
+      const uint32_t odd = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src)) & 3;       // (e8m0: the dword that holds the byte)
+      const __amdgpu_buffer_rsrc_t buf = buffer(src - odd, (static_cast<uint32_t>(t.steps * nb * size) + odd + 3) & ~3u);
+      const int at = (kWindow * n + (lane >> 1)) * nb + min(t.col0 / 128 + (lane & 1), nb - 1);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void*)sm.ws[win], 4, (at * size + odd) & ~3u, 0, 0, 0);
     }
   }
 }
@@ -303,7 +325,7 @@ __device__ __forceinline__ void wide_store(const B128Args& p, const WideTile& t,
                                           rows > 0 && left > 0 ? (rows - 1) * ld + static_cast<uint32_t>(min(left, static_cast<int64_t>(64))) * B : 0u);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const uint32_t row = (16 * i + l15) * ld;
+    const uint32_t row = row_at<KIND>(16 * i + l15) * ld;
     v4f v[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f) v[f] = KIND == kGmmF32 ? acc[i][f] * scale : acc[i][f];
@@ -314,7 +336,7 @@ __device__ __forceinline__ void wide_store(const B128Args& p, const WideTile& t,
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const v4f& a = v[2 * h + (q >> 1)];
-          u[q] = f32_to_bf16(a[2 * (q & 1)]) | static_cast<uint32_t>(f32_to_bf16(a[2 * (q & 1) + 1])) << 16;
+          u[q] = pack_bf16(a[2 * (q & 1)], a[2 * (q & 1) + 1]);
         }
         const int col = 32 * h + 8 * grp;
         __builtin_amdgcn_raw_buffer_store_b128(u, o, col < left ? row + 2 * col : 0xf0000000u, 0, 0);
@@ -346,6 +368,14 @@ struct Stream {
   }
 };
 
+template <int I, int END, class F>
+__device__ __forceinline__ void blocks(const F& f) {
+  if constexpr (I < END) {
+    f(std::integral_constant<int, I>());
+    blocks<I + 1, END>(f);
+  }
+}
+
 // One tile.
 template <Kind KIND, bool OUT_BF16, int MI>
 __device__ __forceinline__ void run_wide(const B128Args& p, WideLds<KIND>& sm, Stream<KIND, OUT_BF16>& st, const WideTile& t, bool stored) {
@@ -361,7 +391,7 @@ __device__ __forceinline__ void run_wide(const B128Args& p, WideLds<KIND>& sm, S
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int f = 0; f < 4; ++f) acc[i][f] = v4f{0.f, 0.f, 0.f, 0.f};
-  uint32_t xsd[MI];                                // gmm: a dword of each row's scales, four blocks
+  uint32_t xsd[KIND == kTgmm ? 2 : MI];            // scales; gmm: a dword of each row's, four blocks; tgmm: a byte a row
   float unit = 1.0f;                               // float32 scales: what the sums are in units of
 #pragma clang loop unroll(disable)
   for (int s = 0; s < t.steps; ++s) {
@@ -394,8 +424,10 @@ __device__ __forceinline__ void run_wide(const B128Args& p, WideLds<KIND>& sm, S
     v8i x[2];
     x[0] = read_x(0);
     if constexpr (KIND == kTgmm) {
-#pragma unroll
-      for (int i = 0; i < MI; ++i) xsd[i] = lds_read<uint8_t>(xsb + 256 * sb + xr + 16 * i);
+      static_assert(MI == 8, "rows of 128");
+      const v2i d = lds_read<v2i>(xsb + 256 * sb + 128 * wr + 8 * l15);
+      xsd[0] = d[0];
+      xsd[1] = d[1];
     } else if ((sb & 3) == 0) {
 #pragma unroll
       for (int i = 0; i < MI; ++i) xsd[i] = lds_read<uint32_t>(xsb + (xr + 16 * i) * kWindow + sb);
@@ -423,6 +455,20 @@ __device__ __forceinline__ void run_wide(const B128Args& p, WideLds<KIND>& sm, S
       unit = m;
       wsc[0] = wsc[1] = wsc[2] = wsc[3] = e;
     }
+    const uint32_t shift = KIND == kTgmm ? 0 : 8 * (sb & 3);
+    auto block = [&](auto i_c) {
+      constexpr int i = decltype(i_c)::value;
+      if (i + 1 < MI) x[(i + 1) & 1] = read_x(i + 1);
+      __builtin_amdgcn_sched_barrier(0);           // (left free, the compiler reads each block's rows behind the last one's products)
+      if constexpr (KIND == kGmmF32) {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) acc[i][f] *= ratio;
+      }
+      const uint32_t xs = KIND == kTgmm ? xsd[(i >> 2) & 1] : xsd[KIND == kTgmm ? 0 : i] >> shift;
+#pragma unroll
+      for (int f = 0; f < 4; ++f) acc[i][f] = mfma_scaled<KIND == kTgmm ? i & 3 : 0>(w[f], wsc[f], x[i & 1], xs, acc[i][f]);
+      __builtin_amdgcn_sched_barrier(0);
+    };
     step_barrier();                                // every wave's weights are read
     if (st.w.more) {
       st.w.load(p, sm, st.count, wave, lane);
@@ -431,20 +477,7 @@ __device__ __forceinline__ void run_wide(const B128Args& p, WideLds<KIND>& sm, S
       st.ahead = false;
     }
     order();
-    const uint32_t shift = KIND == kTgmm ? 0 : 8 * (sb & 3);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      if (i + 1 < MI) x[(i + 1) & 1] = read_x(i + 1);
-      __builtin_amdgcn_sched_barrier(0);           // (left free, the compiler reads each block's rows behind the last one's products)
-      const uint32_t xs = xsd[i] >> shift;
-      if constexpr (KIND == kGmmF32) {
-#pragma unroll
-        for (int f = 0; f < 4; ++f) acc[i][f] *= ratio;
-      }
-#pragma unroll
-      for (int f = 0; f < 4; ++f) acc[i][f] = mfma_scaled(w[f], wsc[f], x[i & 1], xs, acc[i][f]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    blocks<0, MI>(block);
     st.b ^= 1;
     if (last_of_window) st.win ^= 1;
   }
