@@ -185,59 +185,66 @@ struct ColsArgs {
 };
 
 // A workgroup takes 128 rows of one group and every gridDim.y-th 128 of the
-// columns.  A thread holds eight rows of eight columns; a column's maximum goes
-// through LDS, and so do its codes, which leave as one line of 128 bytes.
+// columns, the next ones' loads issued before these are worked on.  A thread
+// holds eight rows of eight columns; a column's maximum goes through LDS, and so
+// do its codes, which leave as one line of 128 bytes.
 template <bool SILU>
 __global__ __launch_bounds__(256) void quantize_cols_b128_kernel(const ColsArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t codes[kBlock * kPitch];
   __shared__ uint32_t tops[16][kBlock + 4];
   __shared__ float invs[kBlock];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int64_t blk = blockIdx.x;
-  const bool says = blk == 0 && blockIdx.y == 0 && tid < 64;
-  if (says) find_block(p.sizes + p.g0, p.El, p.M, INT64_MAX, p.err);    // (a pass over every group, for what is wrong)
-  const GroupBlock f = find_block(p.sizes + p.g0, p.El, p.M, blk, nullptr);
+  const int blk = blockIdx.x;
+  if (blk == 0 && blockIdx.y == 0 && tid < 64)
+    find_block(p.sizes + p.g0, p.El, static_cast<int>(p.M), INT32_MAX, p.err);    // (a pass over every group, for what is wrong)
+  const GroupBlock f = find_block(p.sizes + p.g0, p.El, static_cast<int>(p.M), blk, nullptr);
   if (f.g < 0) return;
-  const int64_t r0 = (blk - f.block0) * kBlock;                          // first row of the block in its group
-  int64_t row[8];
+  const int r0 = (blk - f.block0) * kBlock + 8 * ty;                     // first of the thread's rows in its group
+  const uint16_t *xr[8], *ur[SILU ? 8 : 1];
+  int64_t start = 0;                         // the window's first slot
+  if (p.perm) {
+    for (int g = tid & 63; g < p.g0; g += 64) start += max(p.sizes[g], 0);
+    if (p.g0 > 0)
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) start += __shfl_xor(start, o, 64);
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + 8 * ty + i;
-    row[i] = r < f.m ? f.row0 + r : -1;
+    int64_t row = f.row0 + min(r0 + i, f.m - 1);
+    if (p.perm) row = min(static_cast<int64_t>(max(p.perm[min(start + row, p.T * p.k - 1)], 0)) / p.k, p.T - 1);
+    xr[i] = p.x + row * p.ldx + 8 * tx;
+    if constexpr (SILU) ur[i] = p.x_up + row * p.ldx + 8 * tx;
   }
-  if (p.perm) {
-    int64_t start = 0;                       // the window's first slot
-    for (int g = tid & 63; g < p.g0; g += 64) start += max(p.sizes[g], 0);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) start += __shfl_xor(start, o, 64);
-    const int64_t last = p.T * p.k - 1;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (row[i] >= 0) row[i] = min(static_cast<int64_t>(max(p.perm[min(start + row[i], last)], 0)) / p.k, p.T - 1);
-  }
-  for (int64_t c0 = static_cast<int64_t>(blockIdx.y) * kBlock; c0 < p.C; c0 += static_cast<int64_t>(gridDim.y) * kBlock) {
-    const int64_t c = c0 + 8 * tx;
-    uint4 a[8], b[SILU ? 8 : 1];
+  uint4 a[8], b[SILU ? 8 : 1];
+  const int step = gridDim.y * kBlock;
+  auto load = [&](int c0) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const bool in = row[i] >= 0 && c < p.C;
+      const bool in = r0 + i < f.m && c0 + 8 * tx < p.C;
       a[i] = make_uint4(0, 0, 0, 0);
-      if (in) a[i] = *reinterpret_cast<const uint4*>(p.x + row[i] * p.ldx + c);
+      if (in) a[i] = *reinterpret_cast<const uint4*>(xr[i] + c0);
       if constexpr (SILU) {
         b[i] = make_uint4(0, 0, 0, 0);
-        if (in) b[i] = *reinterpret_cast<const uint4*>(p.x_up + row[i] * p.ldx + c);
+        if (in) b[i] = *reinterpret_cast<const uint4*>(ur[i] + c0);
       }
     }
+  };
+  int c0 = blockIdx.y * kBlock;
+  if (c0 < p.C) load(c0);
+  for (; c0 < p.C; c0 += step) {
     uint32_t top[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    float v[8][8];
+    uint4 raw[8];                            // (plain rows stay as they came: half the registers)
+    float v[SILU ? 8 : 1][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      values8<SILU>(a[i], b[SILU ? i : 0], v[i]);
+      raw[i] = a[i];
+      if constexpr (SILU) values8<true>(a[i], b[i], v[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top[j] = max(top[j], magnitude(v[i][j]));
+      for (int j = 0; j < 8; ++j) top[j] = max(top[j], magnitude(SILU ? v[SILU ? i : 0][j] : Bf16x8{a[i]}.get(j)));
     }
+    if (c0 + step < p.C) load(c0 + step);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) tops[ty][8 * tx + j] = top[j];
+    for (int j = 0; j < 8; j += 4) *reinterpret_cast<uint4*>(&tops[ty][8 * tx + j]) = make_uint4(top[j], top[j + 1], top[j + 2], top[j + 3]);
     __syncthreads();
     if (tid < kBlock) {
       uint32_t t = 0;
@@ -248,21 +255,19 @@ __global__ __launch_bounds__(256) void quantize_cols_b128_kernel(const ColsArgs 
       if (c0 + tid < p.C) p.scale[blk * p.C + c0 + tid] = static_cast<uint8_t>(s);
     }
     __syncthreads();
-    uint2 o[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float u[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = v[i][j];
-      o[j] = encode8(u, invs[8 * tx + j]);
-      *reinterpret_cast<uint2*>(codes + (8 * tx + j) * kPitch + 8 * ty) = o[j];
+      for (int i = 0; i < 8; ++i) u[i] = SILU ? v[SILU ? i : 0][j] : Bf16x8{raw[i]}.get(j);
+      *reinterpret_cast<uint2*>(codes + (8 * tx + j) * kPitch + 8 * ty) = encode8(u, invs[8 * tx + j]);
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int col = (tid >> 3) + 32 * i;
       if (c0 + col < p.C)
-        *reinterpret_cast<uint4*>(p.qt + (c0 + col) * p.cols + blk * kBlock + 16 * (tid & 7)) =
+        *reinterpret_cast<uint4*>(p.qt + (c0 + col) * p.cols + static_cast<int64_t>(blk) * kBlock + 16 * (tid & 7)) =
             *reinterpret_cast<const uint4*>(codes + col * kPitch + 16 * (tid & 7));
     }
     // (the next columns' maxima touch `tops` alone until their first barrier, behind these reads)
@@ -334,7 +339,7 @@ extern "C" int moe_quantize_cols_b128(const void* x, const void* x_up, int64_t l
   // as many blocks as any split of M rows into the groups has
   const int64_t groups = num_local_experts < M ? num_local_experts : M;
   const int64_t blocks = moe_cdiv(M, 128) + groups, tiles = moe_cdiv(C, 128);
-  const int64_t y = moe_cdiv(4096, blocks) < tiles ? moe_cdiv(4096, blocks) : tiles;
+  const int64_t y = moe_cdiv(2560, blocks) < tiles ? moe_cdiv(2560, blocks) : tiles;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(y));
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (act == MOE_ACT_SILU_MUL)

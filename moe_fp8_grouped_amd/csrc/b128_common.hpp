@@ -43,49 +43,55 @@ __device__ __forceinline__ uint2 encode8(const float (&v)[8], float inv) {
 // One group's place among the local groups, by whole blocks of 128 rows.
 struct GroupBlock {
   int g, m;                                  // the local group, and its rows
-  int64_t row0;                              // its first local row
-  int64_t block0;                            // its first block among all groups'
+  int row0;                                  // its first local row
+  int block0;                                // its first block among all groups'
 };
 
+// Inclusive sum over the wave of values from 0 to cap, itself at most cap (which makes it the same in any order): rows of
+// 16 by shifts, then rows into rows, in the vector unit.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int add_from(int v, int cap) {
+  return min(v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false), cap);
+}
+__device__ __forceinline__ int wave_scan(int v, int cap) {
+  v = add_from<0x111, 0xf>(v, cap);          // row_shr 1, 2, 4, 8
+  v = add_from<0x112, 0xf>(v, cap);
+  v = add_from<0x114, 0xf>(v, cap);
+  v = add_from<0x118, 0xf>(v, cap);
+  v = add_from<0x142, 0xa>(v, cap);          // row_bcast 15 into rows 1 and 3, 31 into rows 2 and 3
+  return add_from<0x143, 0xc>(v, cap);
+}
+
 // The group that holds block b (every lane of the wave gets the answer), or
-// g = -1 past the last.  Sizes below zero count as 0, rows past max_rows not
-// at all.  `err` (or NULL) receives what is wrong with the sizes.
-__device__ __forceinline__ GroupBlock find_block(const int32_t* __restrict__ sizes, int El, int64_t max_rows, int64_t b, int32_t* err) {
-  const int lane = threadIdx.x & 63;
-  int64_t rows = 0, blocks = 0;
+// g = -1 past the last.  Sizes below zero count as 0, rows past max_rows (at
+// most 2^23) not at all.  `err` (or NULL) receives what is wrong with the sizes.
+__device__ __forceinline__ GroupBlock find_block(const int32_t* __restrict__ sizes, int El, int max_rows, int b, int32_t* err) {
+  const int lane = threadIdx.x & 63, cap = max_rows + 1;
+  int rows = 0, blocks = 0;
   for (int base = 0; base < El; base += 64) {
     const int raw = base + lane < El ? sizes[base + lane] : 0;
-    const int64_t size = raw < 0 ? 0 : raw;
-    int64_t end = size;                      // inclusive scan of the sizes
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t t = __shfl_up(end, o, 64);
-      if (lane >= o) end += t;
-    }
-    const int64_t r0 = min(rows + end - size, max_rows), r1 = min(rows + end, max_rows);
+    const int size = min(max(raw, 0), cap), before = lane == 0 ? rows : 0;
+    const int end = wave_scan(min(size + before, cap), cap);               // rows up to this group's last
+    const int up = __builtin_amdgcn_update_dpp(rows, end, 0x138, 0xf, 0xf, false);        // wave_shr 1: up to its first
+    const int r0 = min(up, max_rows), r1 = min(end, max_rows);
     if (err) {
       if (raw < 0) raise_error(err, MOE_DEVERR_GROUP_SIZE);
-      if (rows + end > max_rows) raise_error(err, MOE_DEVERR_ROWS);
+      if (end > max_rows) raise_error(err, MOE_DEVERR_ROWS);
     }
-    const int64_t nb = (r1 - r0 + kBlock - 1) / kBlock;
-    int64_t bend = nb;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t t = __shfl_up(bend, o, 64);
-      if (lane >= o) bend += t;
-    }
-    const uint64_t has = __ballot(blocks + bend > b);
+    const int nb = (r1 - r0 + kBlock - 1) / kBlock;
+    const int bend = blocks + wave_scan(nb, cap);                          // (fewer blocks than rows)
+    const uint64_t has = __ballot(bend > b);
     if (has) {
       const int l = __builtin_ctzll(has);
       GroupBlock f;
       f.g = base + l;
-      f.m = static_cast<int>(__shfl(r1 - r0, l, 64));
-      f.row0 = __shfl(r0, l, 64);
-      f.block0 = __shfl(blocks + bend - nb, l, 64);
+      f.m = __builtin_amdgcn_readlane(r1 - r0, l);
+      f.row0 = __builtin_amdgcn_readlane(r0, l);
+      f.block0 = __builtin_amdgcn_readlane(bend - nb, l);
       return f;
     }
-    rows += __shfl(end, 63, 64);
-    blocks += __shfl(bend, 63, 64);
+    rows = __builtin_amdgcn_readlane(end, 63);
+    blocks = __builtin_amdgcn_readlane(bend, 63);
   }
   return GroupBlock{-1, 0, 0, blocks};
 }
