@@ -9,7 +9,7 @@
 //   weights  scale * p_e, or scale * p_e / (sum of the chosen p)
 // A logit of -inf (or NaN) takes its expert out: it is chosen after every
 // other one and its weight is 0.
-#include "common.hpp"
+#include "wave_common.hpp"
 
 namespace moe {
 namespace {
@@ -32,54 +32,6 @@ __device__ __forceinline__ uint32_t order_key(float z) {
 __device__ __forceinline__ uint64_t order_key(double v) {
   const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
   return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
-}
-
-// Reductions over the wave, the same value for every lane: rows of 16 by shifts,
-// then rows into rows, all in the vector unit (through LDS, as a shuffle goes,
-// the k dependent reductions of the choice took most of the kernel's time).
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t dpp(uint32_t none, uint32_t v) {
-  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(none), static_cast<int>(v), CTRL, ROWS, 0xf, false));
-}
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp(float none, float v) {
-  return __uint_as_float(dpp<CTRL, ROWS>(__float_as_uint(none), __float_as_uint(v)));
-}
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double dpp(double none, double v) {
-  const uint64_t n = __double_as_longlong(none), b = __double_as_longlong(v);
-  const uint32_t lo = dpp<CTRL, ROWS>(static_cast<uint32_t>(n), static_cast<uint32_t>(b));
-  const uint32_t hi = dpp<CTRL, ROWS>(static_cast<uint32_t>(n >> 32), static_cast<uint32_t>(b >> 32));
-  return __longlong_as_double(static_cast<int64_t>(hi) << 32 | lo);
-}
-__device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane) {
-  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane));
-}
-__device__ __forceinline__ float from_lane(float v, int lane) { return __uint_as_float(from_lane(__float_as_uint(v), lane)); }
-__device__ __forceinline__ double from_lane(double v, int lane) {
-  const uint64_t b = __double_as_longlong(v);
-  const uint32_t lo = from_lane(static_cast<uint32_t>(b), lane), hi = from_lane(static_cast<uint32_t>(b >> 32), lane);
-  return __longlong_as_double(static_cast<int64_t>(hi) << 32 | lo);
-}
-template <class T, class F>
-__device__ __forceinline__ T over_wave(T v, T none, const F& f) {
-  v = f(v, dpp<0x111, 0xf>(none, v));        // row_shr 1, 2, 4, 8
-  v = f(v, dpp<0x112, 0xf>(none, v));
-  v = f(v, dpp<0x114, 0xf>(none, v));
-  v = f(v, dpp<0x118, 0xf>(none, v));
-  v = f(v, dpp<0x142, 0xa>(none, v));        // row_bcast 15 into rows 1 and 3, 31 into rows 2 and 3
-  v = f(v, dpp<0x143, 0xc>(none, v));
-  return from_lane(v, 63);
-}
-template <class T>
-__device__ __forceinline__ T sum_of(T v) {
-  return over_wave(v, T(0), [](T a, T b) { return a + b; });
-}
-__device__ __forceinline__ float max_of(float v) {
-  return over_wave(v, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
-}
-__device__ __forceinline__ uint32_t max_of(uint32_t v) {
-  return over_wave(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
 
 // Sigmoids of renormalised weights where a chosen logit is below kLow: there
@@ -306,21 +258,6 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(const void* __restrict_
 // 32768 rows of 64 float32 logits, k = 8, 14.0 us against 9.6 as graphs of one
 // call (8.4 in the trace; the bytes alone 3.6; what is left is the launch and
 // instructions).
-__device__ __forceinline__ float row_sum(float v) {   // over sixteen lanes, the same bits for each of them
-  v += dpp<0xB1, 0xf>(0.0f, v);              // lane ^ 1, ^ 2, then halves and rows mirrored
-  v += dpp<0x4E, 0xf>(0.0f, v);
-  v += dpp<0x141, 0xf>(0.0f, v);
-  v += dpp<0x140, 0xf>(0.0f, v);
-  return v;
-}
-__device__ __forceinline__ float row_max(float v) {
-  v = fmaxf(v, dpp<0xB1, 0xf>(0.0f, v));
-  v = fmaxf(v, dpp<0x4E, 0xf>(0.0f, v));
-  v = fmaxf(v, dpp<0x141, 0xf>(0.0f, v));
-  v = fmaxf(v, dpp<0x140, 0xf>(0.0f, v));
-  return v;
-}
-
 template <bool BF16, int V, bool SIGMOID>
 __global__ __launch_bounds__(256) void router_bwd_rows_kernel(const void* __restrict__ logits, int64_t ldl,
                                                               const int32_t* __restrict__ ids,
