@@ -14,7 +14,7 @@ constexpr int kMaxE = 1024, kMaxK = 64;
 constexpr float kOut = -1e30f;               // a logit at or below it, or NaN, takes its expert out
 constexpr int64_t kHeader = 256;             // workspace: error word
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kChunk = 128;                  // tokens of a workgroup of the forward pass, at least
+constexpr int kChunk = 64;                   // tokens of a workgroup of the forward pass, at least: four a wave
 
 // G lanes (16 or the whole wave) share a row, lane `sub` of them holds experts 4 G i + 4 sub .. + 3 for i < V.
 template <bool BF16, int G, int V>
@@ -69,17 +69,21 @@ __device__ __forceinline__ float over_row(float v) {
 // A score up to a factor common to the row, with m its largest logit: exp(z - m), or
 // sigmoid(z) / exp(min(m, 0)) = exp(min(z, 0) - min(m, 0)) / (1 + exp(-|z|)),
 // which stays in range where every sigmoid of the row is below it.  0 for an
-// expert taken out.
+// expert taken out.  (exp and 1 / x by the hardware's operations, within 1 ulp of
+// their argument's: the argument's own rounding, |z - m| half ulps, is the larger
+// part, and a share needs no more than the loss and the gradient hold.)
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
+__device__ __forceinline__ float fast_inverse(float x) { return __builtin_amdgcn_rcpf(x); }
 template <bool SIGMOID>
 __device__ __forceinline__ float score(float z, float m, float& rest) {
   if (z == -INFINITY) return 0.0f;
   if constexpr (SIGMOID) {
-    const float e = expf(-fabsf(z)), d = 1.0f / (1.0f + e);
+    const float e = fast_exp(-fabsf(z)), d = fast_inverse(1.0f + e);
     rest = z < 0.0f ? d : e * d;
-    return (z < 0.0f ? expf(z - fminf(m, 0.0f)) : 1.0f) * d;
+    return (z < 0.0f ? fast_exp(z - fminf(m, 0.0f)) : 1.0f) * d;
   } else {
     rest = 1.0f;
-    return expf(z - m);
+    return fast_exp(z - m);
   }
 }
 
@@ -126,9 +130,8 @@ struct BalanceArgs {
 // slots are a run.)
 template <bool BF16, bool SIGMOID, int G, int V>
 __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs p, int64_t chunk) {
-  constexpr int PER = 64 / G, U = V >= 2 && G == 64 ? 2 : 4;             // rows a wave at a time, and how often before they are used
-  constexpr int PARTS = G == 16 ? 8 : 4;                                 // parts of the sums that go through LDS at a time
-  __shared__ float sums[PARTS][4 * G * V];
+  constexpr int PER = 64 / G, U = G == 16 ? 1 : V >= 2 ? 2 : 4;          // rows a wave at a time, and how often before they are used
+  __shared__ __attribute__((aligned(16))) float sums[kWaves][4 * G * V];
   __shared__ int counts[4 * G * V], tokens;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, sub = lane & (G - 1), E = p.E;
   const int64_t slots = gridDim.x + static_cast<int64_t>(p.S);
@@ -156,15 +159,20 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs p, 
     int n = 0;
     for (int64_t r0 = t + wave * PER * U; r0 < end; r0 += kWaves * PER * U) {
       Row<BF16, G, V> row[U];
+      const int rows = static_cast<int>(min(end - r0, static_cast<int64_t>(PER * U)));
+      // the first 64 choices and their logits beside the rows, any more behind them
+      const int id0 = lane < rows * p.k ? p.ids[r0 * p.k + lane] : -1;
 #pragma unroll
       for (int u = 0; u < U; ++u) row[u].load(p.z, min(r0 + u * PER + lane / G, end - 1) * p.ldl, E, sub, p.wide);
-      const int rows = static_cast<int>(min(end - r0, static_cast<int64_t>(PER * U)));
-      for (int j = lane; j < rows * p.k; j += 64) {
-        const int64_t r = r0 + j / p.k;
+      auto logit = [&](int j, int id) {
+        const int64_t at = (r0 + j / p.k) * p.ldl + id;
+        return BF16 ? bf16_to_f32(static_cast<const uint16_t*>(p.z)[at]) : static_cast<const float*>(p.z)[at];
+      };
+      const bool in0 = id0 >= 0 && id0 < E;
+      const float z0 = in0 ? logit(lane, id0) : -INFINITY;
+      for (int j = 64 + lane; j < rows * p.k; j += 64) {
         const int id = p.ids[r0 * p.k + j];
-        if (id < 0 || id >= E) continue;
-        const float z = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(p.z)[r * p.ldl + id]) : static_cast<const float*>(p.z)[r * p.ldl + id];
-        if (z > kOut) atomicAdd(&counts[id], 1);
+        if (id >= 0 && id < E && logit(j, id) > kOut) atomicAdd(&counts[id], 1);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -178,41 +186,35 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs p, 
             q[i][c] = score<SIGMOID>(row[u].z[i][c], m, rest);
             sum += q[i][c];
           }
-        const float inv = 1.0f / over_row<G>(sum);
+        const float inv = fast_inverse(over_row<G>(sum));
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[i][c] = fmaf(q[i][c], inv, acc[i][c]);
         ++n;
       }
+      if (z0 > kOut) atomicAdd(&counts[id0], 1);
     }
     if (sub == 0 && n) atomicAdd(&tokens, n);
-    // the sums of all rows' lanes, in order
+    // the sums of the waves, in order (of a wave's rows of lanes first)
     const int64_t slot = blockIdx.x + static_cast<int64_t>(s);
-    float total[(4 * G * V + kThreads - 1) / kThreads];
 #pragma unroll
-    for (int j = 0; j < (4 * G * V + kThreads - 1) / kThreads; ++j) total[j] = 0.0f;
-    const int own = wave * PER + lane / G;
-    for (int first = 0; first < kWaves * PER; first += PARTS) {
-      if (own >= first && own < first + PARTS)
+    for (int i = 0; i < V; ++i) {
+      if (G == 16)
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          *reinterpret_cast<float4*>(&sums[own - first][4 * G * i + 4 * sub]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < (4 * G * V + kThreads - 1) / kThreads; ++j)
-        if (tid + j * kThreads < E)
-#pragma unroll
-          for (int q = 0; q < PARTS; ++q) total[j] += sums[q][tid + j * kThreads];
-      __syncthreads();
+        for (int c = 0; c < 4; ++c) {
+          acc[i][c] += __shfl_xor(acc[i][c], 16, 64);
+          acc[i][c] += __shfl_xor(acc[i][c], 32, 64);
+        }
+      if (lane < G) *reinterpret_cast<float4*>(&sums[wave][4 * G * i + 4 * sub]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
     }
+    __syncthreads();
+    if (tid < E) {                           // (E <= kThreads)
+      float total = 0.0f;
 #pragma unroll
-    for (int j = 0; j < (4 * G * V + kThreads - 1) / kThreads; ++j) {
-      const int e = tid + j * kThreads;
-      if (e < E) {
-        part[slot * E + e] = total[j];
-        cpart[slot * E + e] = counts[e];
-      }
+      for (int q = 0; q < kWaves; ++q) total += sums[q][tid];
+      part[slot * E + tid] = total;
+      cpart[slot * E + tid] = counts[tid];
     }
     if (tid == 0) npart[slot] = tokens;
     __syncthreads();
@@ -339,7 +341,7 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(const BalanceArgs p, c
       }
     sum = over_row<G>(sum);
     dot = over_row<G>(dot);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum > 0.0f ? fast_inverse(sum) : 0.0f;
     if (!in) continue;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
