@@ -73,100 +73,114 @@ __device__ __forceinline__ void zero_rows(const B128Args& p, int64_t n_rows) {
     *reinterpret_cast<uint4*>(z + i) = make_uint4(0, 0, 0, 0);
 }
 
-// ------------------------------------------------------------ 16 x 16 tiles
-// A workgroup takes one tile, the contraction's blocks dealt out to its waves,
-// whose sums are added in wave order.
+// ---------------------------------------------------------------- few rows
+// 16 MI rows by 16 columns a workgroup: the weights of sixteen columns are a
+// stream of K bytes each, its blocks dealt out to eight waves, a wave's loads of
+// several blocks issued before their products, and the waves' sums added in wave
+// order.  For decoding: every weight is met by a row or a few, and what counts is to
+// have its bytes under way at once.
 constexpr int kSplit = 8;
 
-struct SmallLds {
-  GroupTable gt;
-  int tmp[kMaxLocal];
-  v4f part[kSplit][64];
-};
-
-template <Kind KIND, bool OUT_BF16>
-__global__ __launch_bounds__(64 * kSplit) void b128_small_kernel(const B128Args p) {
-  __shared__ SmallLds sm;
+template <Kind KIND, bool OUT_BF16, int MI>
+__global__ __launch_bounds__(64 * kSplit) void b128_few_kernel(const B128Args p, int tiles) {
+  constexpr int AHEAD = MI == 1 ? 8 : MI == 2 ? 4 : 2;                   // blocks loaded before their products
+  __shared__ v4f part[kSplit][MI][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l15 = lane & 15, grp = lane >> 4;
-  const int NT = static_cast<int>(p.N / 16), KT = static_cast<int>(p.K / 16);
-  constexpr bool TG = KIND == kTgmm;
-  // gmm: a group's row tiles by column tiles; tgmm: every group's K by N tiles (the table then counts its 128-row blocks)
-  build_groups(p.sizes, p.g0, p.El, p.M, TG ? 1 : NT, TG ? b128::kBlock : 16, p.err, sm.gt, sm.tmp);
-  const int64_t total = TG ? static_cast<int64_t>(p.El) * KT * NT : sm.gt.tiles_off[p.El];
-  for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
-    int g, rows;
-    int64_t row0, col0, wrow0;
-    int kb, kend;                                  // blocks of the contraction, and its end in bytes
-    const uint8_t *xp, *wp;
-    int64_t ldx, ldw;
-    if (TG) {
-      g = static_cast<int>(t / (static_cast<int64_t>(KT) * NT));
-      const int64_t l = t - static_cast<int64_t>(g) * KT * NT;
-      row0 = 16 * (l / NT);
-      col0 = 16 * (l % NT);
-      rows = 16;
-      wrow0 = col0;
-      kb = sm.gt.tiles_off[g + 1] - sm.gt.tiles_off[g];
-      kend = kb * 128;
-      ldx = ldw = p.ldx;
-      xp = p.x + static_cast<int64_t>(sm.gt.tiles_off[g]) * 128;
-      wp = p.w + static_cast<int64_t>(sm.gt.tiles_off[g]) * 128;
-    } else {
-      g = find_group(sm.gt, p.El, static_cast<int>(t));
-      const int m = sm.gt.rows_off[g + 1] - sm.gt.rows_off[g], l = static_cast<int>(t) - sm.gt.tiles_off[g], nr = (m + 15) / 16;
-      row0 = sm.gt.rows_off[g] + 16 * (l % nr);
-      rows = min(16, m - 16 * (l % nr));
-      col0 = 16 * (l / nr);
-      wrow0 = static_cast<int64_t>(g) * p.N + col0;
-      kend = static_cast<int>(p.K);
-      kb = (kend + 127) / 128;
-      ldx = p.ldx;
-      ldw = p.K;
-      xp = p.x;
-      wp = p.w;
-    }
-    const int64_t xrow = row0 + min(l15, rows - 1);
-    const uint8_t* xa = xp + xrow * ldx;
-    const uint8_t* wa = wp + (wrow0 + l15) * ldw;
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
-    const int per = (kb + kSplit - 1) / kSplit;
-    for (int b = wave * per; b < min(kb, (wave + 1) * per); ++b) {
-      uint4 xv[2], wv[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int at = 128 * b + 64 * h + 16 * grp;
-        xv[h] = wv[h] = make_uint4(0, 0, 0, 0);
-        if (at < kend) {
-          xv[h] = *reinterpret_cast<const uint4*>(xa + at);
-          wv[h] = *reinterpret_cast<const uint4*>(wa + at);
-        }
+  const int NT = static_cast<int>(p.N / 16), M = static_cast<int>(p.M);
+  const int j = blockIdx.x / NT, ct = blockIdx.x - j * NT;
+  int g = 0, row0 = 16 * MI * j, rows, there;      // the tile's group and rows; rows that there are to load
+  if (p.El == 1) {                                 // nothing but the store waits for the size
+    const int m = p.sizes[p.g0];
+    if (blockIdx.x == 0 && tid == 0 && m < 0) raise_error(p.err, MOE_DEVERR_GROUP_SIZE);
+    if (blockIdx.x == 0 && tid == 0 && m > M) raise_error(p.err, MOE_DEVERR_ROWS);
+    rows = min(m, M) - row0;
+    there = M - row0;
+  } else {                                         // the group that holds row tile j, of `tiles` - 1 at most
+    const bool tell = j == tiles - 1 && ct == 0 && wave == 0;            // (the last tile is nobody's: it meets every size)
+    int have = 0, before = 0;
+    bool found = false;
+    for (int base = 0; base < p.El && !found; base += 64) {
+      const int raw = base + lane < p.El ? p.sizes[p.g0 + base + lane] : 0;
+      const int end = b128::wave_scan(min(min(max(raw, 0), M) + (lane == 0 ? have : 0), M), M);      // rows up to this group's last
+      const int up = __builtin_amdgcn_update_dpp(have, end, 0x138, 0xf, 0xf, false);                 // wave_shr 1: up to its first
+      if (tell && raw < 0) raise_error(p.err, MOE_DEVERR_GROUP_SIZE);
+      if (tell && raw > M - up) raise_error(p.err, MOE_DEVERR_ROWS);
+      const int n = (end - up + 16 * MI - 1) / (16 * MI), last = before + b128::wave_scan(n, M);
+      const uint64_t has = __ballot(last > j);
+      if (has) {
+        const int l = __builtin_ctzll(has), at = 16 * MI * (j - __builtin_amdgcn_readlane(last - n, l));
+        found = true;
+        g = base + l;
+        row0 = __builtin_amdgcn_readlane(up, l) + at;
+        rows = __builtin_amdgcn_readlane(end - up, l) - at;
       }
-      if constexpr (TG) {
-        const int64_t blk = sm.gt.tiles_off[g] + b;
-        acc = mfma_scaled(frag(wv[0], wv[1]), static_cast<const uint8_t*>(p.ws)[blk * p.N + wrow0 + l15], frag(xv[0], xv[1]),
-                          p.xs[blk * p.K + xrow], acc);
-      } else {
-        const int64_t nb = (p.N + 127) / 128, at = (static_cast<int64_t>(g) * kb + b) * nb + col0 / 128;
-        const uint32_t xs = p.xs[xrow * p.lds + b];
-        if constexpr (KIND == kGmmE8M0)
-          acc = mfma_scaled(frag(wv[0], wv[1]), static_cast<const uint8_t*>(p.ws)[at], frag(xv[0], xv[1]), xs, acc);
+      have = __builtin_amdgcn_readlane(end, 63);
+      before = __builtin_amdgcn_readlane(last, 63);
+    }
+    if (!found) {                                  // rows past the last group's are zero
+      if (j == tiles - 1)
+        for (int i = tid; i < 4 * (M - have); i += 64 * kSplit) store4<OUT_BF16>(p.out, (have + (i >> 2)) * p.N + 16 * ct + 4 * (i & 3), v4f{0.f, 0.f, 0.f, 0.f});
+      return;
+    }
+    there = rows;
+  }
+  const uint32_t K = static_cast<uint32_t>(p.K), ldx = static_cast<uint32_t>(p.ldx);
+  const int kb = static_cast<int>((K + 127) / 128), nb = static_cast<int>((p.N + 127) / 128);
+  const __amdgpu_buffer_rsrc_t xbuf = buffer(p.x + row0 * p.ldx, (min(there, 16 * MI) - 1) * ldx + K);
+  const __amdgpu_buffer_rsrc_t wbuf = buffer(p.w + (static_cast<int64_t>(g) * p.N + 16 * ct) * p.K, 16 * K);
+  const uint8_t* xs = p.xs + (row0 + static_cast<int64_t>(min(l15, there - 1))) * p.lds;
+  const int64_t ws0 = static_cast<int64_t>(g) * kb * nb + ct / 8;
+  v4f acc[MI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+  const int per = (kb + kSplit - 1) / kSplit, end = min(kb, (wave + 1) * per);
+  for (int b0 = wave * per; b0 < end; b0 += AHEAD) {
+    uint4 w[AHEAD][2], x[AHEAD][MI][2];
+    uint32_t xsc[AHEAD][MI], wsc[AHEAD];
+    float wf[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      if (b0 + u >= end) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {                // chunks past K, and rows past those there are, lie outside the buffers: zeros
+        const uint32_t at = 128u * (b0 + u) + 64 * h + 16 * grp, o = at < K ? at : 0x80000000u;
+        w[u][h] = buffer_load16(wbuf, l15 * K + o, 0);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) x[u][i][h] = buffer_load16(xbuf, (16 * i + l15) * ldx + o, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i) xsc[u][i] = 16 * i + l15 < there ? xs[16 * i * p.lds + b0 + u] : 0;
+      const int64_t at = ws0 + static_cast<int64_t>(b0 + u) * nb;
+      if (KIND == kGmmF32)
+        wf[u] = static_cast<const float*>(p.ws)[at];
+      else
+        wsc[u] = static_cast<const uint8_t*>(p.ws)[at];
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      if (b0 + u >= end) continue;
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const v8i wv = frag(w[u][0], w[u][1]), xv = frag(x[u][i][0], x[u][i][1]);
+        if constexpr (KIND == kGmmF32)
+          acc[i] += wf[u] * mfma_scaled(wv, 127, xv, xsc[u][i], v4f{0.f, 0.f, 0.f, 0.f});
         else
-          acc += static_cast<const float*>(p.ws)[at] * mfma_scaled(frag(wv[0], wv[1]), 127, frag(xv[0], xv[1]), xs, v4f{0.f, 0.f, 0.f, 0.f});
+          acc[i] = mfma_scaled(wv, wsc[u], xv, xsc[u][i], acc[i]);
       }
-    }
-    __syncthreads();
-    sm.part[wave][lane] = acc;
-    __syncthreads();
-    if (wave == 0) {
-      acc = sm.part[0][lane];
-#pragma unroll
-      for (int i = 1; i < kSplit; ++i) acc += sm.part[i][lane];
-      if (l15 < rows)
-        store4<OUT_BF16>(p.out, (TG ? static_cast<int64_t>(g) * p.K + row0 + l15 : row0 + l15) * p.N + col0 + 4 * grp, acc);
     }
   }
-  if constexpr (!TG) zero_rows<OUT_BF16, 64 * kSplit>(p, sm.gt.rows_off[p.El]);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) part[wave][i][lane] = acc[i];
+  __syncthreads();
+  const int r = 16 * wave + l15;
+  if (wave < MI && r < (p.El == 1 ? there : rows)) {
+    v4f sum = part[0][wave][lane];
+#pragma unroll
+    for (int i = 1; i < kSplit; ++i) sum += part[i][wave][lane];
+    if (r >= rows) sum = v4f{0.f, 0.f, 0.f, 0.f};
+    store4<OUT_BF16>(p.out, (row0 + static_cast<int64_t>(r)) * p.N + 16 * ct + 4 * grp, sum);
+  }
 }
 
 // ---------------------------------------------------------------- wide tiles
@@ -585,14 +599,260 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_wide_kernel(const B128Ar
   if constexpr (!TG) zero_rows<OUT_BF16, kWideThreads>(p, n_rows);
 }
 
+// ---------------------------------------------------------------- narrow tiles
+// 64 x 64 results a workgroup of eight waves, four by two, each 16 rows by 32
+// columns; eight stages of both operands in LDS, seven ahead, the stream running on from
+// tile to tile: for fewer rows or tiles than the wide ones fill the GPU with, where
+// the loads' latency is the time.  Each stage brings its scales.
+constexpr int kNarrow = 64, kNarrowStages = 8, kNarrowDesc = 256;
+
+struct NarrowLds {
+  uint8_t x[kNarrowStages][kNarrow * 128];
+  uint8_t w[kNarrowStages][kNarrow * 128];
+  uint32_t xs[kNarrowStages][kNarrow];             // gmm: the dword of each row that holds the block's byte; tgmm: 64 bytes
+  uint32_t ws[kNarrowStages][kNarrow];             // gmm: one dword; tgmm: 64 bytes
+  int4 desc[kNarrowDesc];                          // first row, column tile, group, rows
+  int2 more[kNarrowDesc];                          // blocks, first block
+};
+static_assert(sizeof(NarrowLds) <= 160 * 1024, "LDS of a CU");
+
+__device__ __forceinline__ WideTile narrow_tile(const NarrowLds& sm, int i) {
+  WideTile t = wide_tile(sm, i);
+  t.col0 = t.col0 / kWideCols * kNarrow;
+  return t;
+}
+
+template <Kind KIND, bool OUT_BF16>
+__global__ __launch_bounds__(kWideThreads, 2) void b128_narrow_kernel(const B128Args p) {
+  __shared__ __attribute__((aligned(1024))) NarrowLds sm;
+  constexpr bool TG = KIND == kTgmm;
+  constexpr int NST = kNarrowStages;
+  const int NT = static_cast<int>((p.N + kNarrow - 1) / kNarrow), RT = TG ? static_cast<int>((p.K + kNarrow - 1) / kNarrow) : 0;
+  // the group table lives in the stages while tiles are decoded, up to kNarrowDesc at a time
+  struct Table {
+    int rows_off[kMaxLocal + 1], tiles_off[kMaxLocal + 1], blocks_off[kMaxLocal + 1], tmp[kMaxLocal];
+  };
+  static_assert(sizeof(Table) <= sizeof(sm.x), "the group table fits the stages");
+  Table& gt = *reinterpret_cast<Table*>(&sm.x[0][0]);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l15 = lane & 15, grp = lane >> 4, wr = wave >> 1, wc = wave & 1;
+  const int nb = static_cast<int>((p.N + 127) / 128);
+  int first = 0, last = 0, step = 1, n_rows = 0;
+#pragma clang loop unroll(disable)
+  for (int base = 0;; base += kNarrowDesc) {
+    __syncthreads();
+    for (int g = tid; g < p.El; g += kWideThreads) {
+      int m = p.sizes[p.g0 + g];
+      if (m < 0) {
+        if (blockIdx.x == 0) raise_error(p.err, MOE_DEVERR_GROUP_SIZE);
+        m = 0;
+      }
+      gt.tmp[g] = m;
+    }
+    __syncthreads();
+    const bool over = wave0_scan_sat(gt.tmp, gt.rows_off, p.El, p.M);
+    if (over && tid == 0 && blockIdx.x == 0) raise_error(p.err, MOE_DEVERR_ROWS);
+    __syncthreads();
+    for (int g = tid; g < p.El; g += kWideThreads) {
+      const int m = gt.rows_off[g + 1] - gt.rows_off[g];
+      gt.tmp[g] = TG ? (m + 127) / 128 : row_tiles(m, kNarrow) * NT;
+    }
+    __syncthreads();
+    wave0_scan(gt.tmp, TG ? gt.blocks_off : gt.tiles_off, p.El);
+    __syncthreads();
+    xcd_share(TG ? p.El * RT * NT : gt.tiles_off[p.El], first, last, step);
+    n_rows = gt.rows_off[p.El];
+    const int left = first < last ? (last - first + step - 1) / step - base : 0;       // this workgroup's tiles
+    const int count = min(left, kNarrowDesc);
+    if (tid < count) {
+      const int t = first + (base + tid) * step;
+      if (TG) {
+        const int g = t / (RT * NT), l = t - g * RT * NT, rt = l / NT, ct = l - rt * NT;
+        sm.desc[tid] = make_int4(kNarrow * rt, ct, g, min(kNarrow, static_cast<int>(p.K) - kNarrow * rt));
+        sm.more[tid] = make_int2(gt.blocks_off[g + 1] - gt.blocks_off[g], gt.blocks_off[g]);
+      } else {
+        const int g = find_group(gt, p.El, t);
+        const int m = gt.rows_off[g + 1] - gt.rows_off[g], nr = row_tiles(m, kNarrow), fr = tile_frags(m, nr);
+        const int local = t - gt.tiles_off[g], ct = local / nr, rt = local - ct * nr;
+        const int rows = max(min(16 * fr, m - 16 * fr * rt), 0);
+        sm.desc[tid] = make_int4(gt.rows_off[g] + 16 * fr * rt, ct, g, rows);
+        sm.more[tid] = make_int2(rows ? static_cast<int>((p.K + 127) / 128) : 0, 0);
+      }
+    }
+    __syncthreads();
+    // the loads' place in the stream
+    WideTile lt{};
+    int li = 0, ls = 0, lb = 0, issued = 0;
+    __amdgpu_buffer_rsrc_t xbuf = buffer(p.x, 0), wbuf = xbuf, xsbuf = xbuf, wsbuf = xbuf;
+    uint32_t odd = 0;
+    auto seek = [&] {
+      ls = 0;
+      for (; li < count; ++li) {
+        lt = narrow_tile(sm, li);
+        if (lt.steps > 0) break;
+      }
+      if (li >= count) return;
+      const uint32_t cols = static_cast<uint32_t>(min(static_cast<int>(p.N) - lt.col0, kNarrow));
+      if constexpr (TG) {
+        const uint32_t len = 128u * lt.steps, ld = static_cast<uint32_t>(p.ldx);
+        const int64_t at = 128 * static_cast<int64_t>(lt.blk0);
+        xbuf = buffer(p.x + static_cast<int64_t>(lt.row0) * p.ldx + at, (lt.rows - 1) * ld + len);
+        wbuf = buffer(p.w + static_cast<int64_t>(lt.col0) * p.ldx + at, (cols - 1) * ld + len);
+      } else {
+        const uint32_t K = static_cast<uint32_t>(p.K), lds = static_cast<uint32_t>(p.lds);
+        xbuf = buffer(p.x + static_cast<int64_t>(lt.row0) * p.ldx, (lt.rows - 1) * static_cast<uint32_t>(p.ldx) + K);
+        wbuf = buffer(p.w + (static_cast<int64_t>(lt.g) * p.N + lt.col0) * p.K, cols * K);
+        xsbuf = buffer(p.xs + lt.row0 * p.lds, lt.rows * lds);
+        const int size = KIND == kGmmF32 ? 4 : 1;
+        const uint8_t* src = static_cast<const uint8_t*>(p.ws) + (static_cast<int64_t>(lt.g) * lt.steps * nb + lt.col0 / 128) * size;
+        odd = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src)) & 3;
+        wsbuf = buffer(src - odd, (static_cast<uint32_t>(lt.steps * nb * size) + odd + 3) & ~3u);
+      }
+    };
+    const int lr = 8 * wave + (lane >> 3);         // the staged row that the lane fills
+    const uint32_t ldx = static_cast<uint32_t>(p.ldx), ldw = static_cast<uint32_t>(TG ? p.ldx : p.K);
+    const uint32_t xc = 16 * ((lane & 7) ^ swz_run(lr)), wch = 16 * ((lane & 7) ^ (OUT_BF16 ? swz_quads(lr) : swz_run(lr)));
+    // one load of each operand a wave; waves 0 and 1 bring the scales as well
+    auto load = [&] {
+      uint32_t xo = lr * ldx + xc, wo = lr * ldw + wch;
+      if (!TG && 128 * ls + 128 > p.K) {
+        const uint32_t end = static_cast<uint32_t>(p.K) - 128u * ls;
+        xo = xc < end ? xo : 0x80000000u;
+        wo = wch < end ? wo : 0x80000000u;
+      }
+      if (wave == 0) {
+        if constexpr (TG) {
+          const __amdgpu_buffer_rsrc_t b = buffer(p.xs + (static_cast<int64_t>(lt.blk0) + ls) * p.K + lt.row0, static_cast<uint32_t>(lt.rows));
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)sm.xs[lb], 4, 4 * lane, 0, 0, 0);
+        } else {
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(xsbuf, (lds_void*)sm.xs[lb], 4, lane * static_cast<uint32_t>(p.lds), ls & ~3, 0, 0);
+        }
+      } else if (wave == 1) {
+        if constexpr (TG) {
+          const __amdgpu_buffer_rsrc_t b = buffer(static_cast<const uint8_t*>(p.ws) + (static_cast<int64_t>(lt.blk0) + ls) * p.N + lt.col0,
+                                                  static_cast<uint32_t>(min(static_cast<int>(p.N) - lt.col0, kNarrow)));
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)sm.ws[lb], 4, 4 * lane, 0, 0, 0);
+        } else {
+          const uint32_t at = KIND == kGmmF32 ? 4u * ls * nb : (odd + ls * nb) & ~3u;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(wsbuf, (lds_void*)sm.ws[lb], 4, at, 0, 0, 0);
+        }
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wbuf, (lds_void*)(sm.w[lb] + 1024 * wave), 16, wo, 128u * ls, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xbuf, (lds_void*)(sm.x[lb] + 1024 * wave), 16, xo, 128u * ls, 0, 0);
+      order();
+      lb = lb + 1 == NST ? 0 : lb + 1;
+      ++issued;
+      if (++ls == lt.steps) {
+        ++li;
+        seek();
+      }
+    };
+    seek();
+#pragma unroll
+    for (int j = 0; j < NST - 1; ++j)
+      if (li < count) load();
+    const int wrow = 32 * wc + frag_col<OUT_BF16>(0, l15);
+    const uint32_t xa0 = lds_addr(sm.x[0]) + (16 * wr + l15) * 128 + 16 * (grp ^ swz_run(l15));
+    const uint32_t wa0 = lds_addr(sm.w[0]) + wrow * 128 + 16 * (grp ^ (OUT_BF16 ? swz_quads(wrow) : swz_run(wrow)));
+    int done = 0, b = 0;
+#pragma clang loop unroll(disable)
+    for (int i = 0; i < count; ++i) {
+      const WideTile t = narrow_tile(sm, i);
+      v4f acc[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
+#pragma clang loop unroll(disable)
+      for (int s = 0; s < t.steps; ++s) {
+        // the stage is there when at most the six behind it are outstanding (and what was stored before them)
+        if (issued - done < NST - 1)
+          __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        else if (wave < 2)
+          __builtin_amdgcn_s_waitcnt(waitcnt_vm(3 * (NST - 2)));
+        else
+          __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * (NST - 2)));
+        step_barrier();                            // every wave's loads are; the stage before is read
+        if (li < count) load();
+        ++done;
+        if (16 * wr < t.rows) {
+          const uint32_t xa = xa0 + b * static_cast<uint32_t>(sizeof(sm.x[0])), wa = wa0 + b * static_cast<uint32_t>(sizeof(sm.w[0]));
+          const v8i x = frag(__builtin_bit_cast(uint4, lds_read<v4i>(xa)), __builtin_bit_cast(uint4, lds_read<v4i>(xa ^ 64u)));
+          const uint32_t xsa = lds_addr(sm.xs[0]) + b * static_cast<uint32_t>(sizeof(sm.xs[0])), wsa = lds_addr(sm.ws[0]) + b * static_cast<uint32_t>(sizeof(sm.ws[0]));
+          uint32_t xs, ws[2];
+          float wf = 1.0f;
+          if constexpr (TG) {
+            xs = lds_read<uint8_t>(xsa + 16 * wr + l15);
+#pragma unroll
+            for (int f = 0; f < 2; ++f) ws[f] = lds_read<uint8_t>(wsa + wrow + frag_col<OUT_BF16>(f, 0));
+          } else {
+            xs = lds_read<uint32_t>(xsa + 4 * (16 * wr + l15)) >> (8 * (s & 3));
+            if constexpr (KIND == kGmmF32) {
+              wf = lds_read<float>(wsa);
+              ws[0] = ws[1] = 127;
+            } else {
+              const uint32_t byte = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.ws)) + (static_cast<uint32_t>(t.g) * t.steps + s) * nb + t.col0 / 128) & 3;
+              ws[0] = ws[1] = lds_read<uint8_t>(wsa + byte);
+            }
+          }
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const uint32_t at = frag_col<OUT_BF16>(f, 0) * 128;
+            const v8i w = frag(__builtin_bit_cast(uint4, lds_read<v4i>(wa + at)), __builtin_bit_cast(uint4, lds_read<v4i>((wa ^ 64u) + at)));
+            if constexpr (KIND == kGmmF32)
+              acc[f] += wf * mfma_scaled(w, 127, x, xs, v4f{0.f, 0.f, 0.f, 0.f});
+            else
+              acc[f] = mfma_scaled(w, ws[f], x, xs, acc[f]);
+          }
+        }
+        b = b + 1 == NST ? 0 : b + 1;
+      }
+      if (16 * wr + l15 < t.rows) {
+        const int64_t row = (TG ? t.g * p.K + t.row0 : t.row0) + 16 * wr + l15;
+        if (OUT_BF16) {
+          const int64_t c = t.col0 + 32 * wc + 8 * grp;
+          if (c < p.N)
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.N + c) =
+                make_uint4(pack_bf16(acc[0][0], acc[0][1]), pack_bf16(acc[0][2], acc[0][3]), pack_bf16(acc[1][0], acc[1][1]), pack_bf16(acc[1][2], acc[1][3]));
+        } else {
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const int64_t c = t.col0 + 32 * wc + 16 * f + 4 * grp;
+            if (c < p.N) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.N + c) = make_float4(acc[f][0], acc[f][1], acc[f][2], acc[f][3]);
+          }
+        }
+      }
+    }
+    if (left <= kNarrowDesc) break;
+  }
+  if constexpr (!TG) zero_rows<OUT_BF16, kWideThreads>(p, n_rows);
+}
+
+// Workgroups of the few-rows kernel with 16 MI rows a tile.
+template <int MI>
+int64_t few_tiles(const B128Args& p) {
+  const int64_t groups = p.El < p.M ? p.El : p.M;
+  return p.El == 1 ? moe_cdiv(p.M, 16 * MI) : p.M / (16 * MI) + groups + 1;
+}
+template <Kind KIND, bool OUT_BF16, int MI>
+bool few(const B128Args& p, hipStream_t st) {
+  const int64_t tiles = few_tiles<MI>(p), grid = tiles * (p.N / 16);
+  // As long as its 16 x 16 pieces are at most six a CU.  One group of 7168 by 4096: 1 row 8.2 us (narrow tiles 27), 64 rows
+  // 23 (33), 128 rows 42 (33); 64 groups of 2048 by 1536: 8 rows 11 (12), 16 rows 19 (19), 32 rows 31 (26).
+  if (grid * MI > 6 * num_cus()) return false;
+  b128_few_kernel<KIND, OUT_BF16, MI><<<static_cast<unsigned>(grid), 64 * kSplit, 0, st>>>(p, static_cast<int>(tiles));
+  return true;
+}
+
 template <Kind KIND, bool OUT_BF16>
 hipError_t launch_b128(const B128Args& p, hipStream_t st) {
   const int64_t groups = p.El < p.M ? p.El : p.M, cols = moe_cdiv(p.N, kWideCols);
   const int64_t tiles = KIND == kTgmm ? p.El * moe_cdiv(p.K, kWideRows<KIND>) * cols : (groups + p.M / kWideRows<KIND>) * cols;
+  if constexpr (KIND != kTgmm) {
+    const bool one = p.El == 1;
+    if (one && p.M > 32 ? few<KIND, OUT_BF16, 4>(p, st) : one && p.M > 16 ? few<KIND, OUT_BF16, 2>(p, st) : few<KIND, OUT_BF16, 1>(p, st))
+      return hipGetLastError();
+  }
   if (tiles >= num_cus())
     b128_wide_kernel<KIND, OUT_BF16><<<num_cus(), kWideThreads, 0, st>>>(p);
   else
-    b128_small_kernel<KIND, OUT_BF16><<<4 * num_cus(), 64 * kSplit, 0, st>>>(p);
+    b128_narrow_kernel<KIND, OUT_BF16><<<num_cus(), kWideThreads, 0, st>>>(p);
   return hipGetLastError();
 }
 
