@@ -12,6 +12,8 @@ W^T) and dW = tgmm(X, dY).
 RoutedFFN starts at the router's logits, with 4-bit expert weights: router ->
 the steps above over the microscaled 4-bit format -> gather-reduce, or, for a
 few tokens, router -> the whole layer in one call; and the router's gradient.
+BlockScaledFFN is a training step of that layer in e4m3 with a scale for every
+block of 128: the forward pass, the router's balance loss, and every gradient.
 
 Expert parallelism is modelled as one GPU's slice: experts
 [group_offset, group_offset + num_local_experts) are local; the sorted
@@ -24,14 +26,16 @@ are quantized once at setup.
 import numpy as np
 import torch
 
-from . import (MOE_ACT_NONE, MOE_ACT_SILU_MUL, MOE_BF16, MOE_E4M3FN, MOE_F32, MOE_MX4, MOE_OP_FFN_TOKENS,
-               MOE_OP_GATHER_REDUCE, MOE_OP_GMM, MOE_OP_GMM_MX4, MOE_OP_QUANTIZE_ROWS, MOE_OP_SORT_BY_EXPERT, MOE_OP_TGMM,
-               MOE_SCALE_ROW_DYNAMIC, MOE_SCALE_TENSOR_DYNAMIC, MOE_SCALE_TENSOR_FROM_ROW_AMAX, MOE_SCALE_TENSOR_STATIC,
-               MOE_SCORE_SOFTMAX, moe_ffn_tokens, moe_gather_reduce, moe_gather_reduce_backward, moe_gmm_fp8,
-               moe_gmm_mx4, moe_quantize_rows, moe_quantize_rows_mx4, moe_quantize_rows_strided,
-               moe_quantize_sort_by_expert, moe_quantize_weights, moe_quantize_weights_mx4, moe_router_topk,
-               moe_router_topk_backward, moe_silu_mul_backward, moe_sort_by_expert, moe_sort_gather_transposed,
-               moe_tgmm_fp8, moe_tgmm_fp8_xt, tgmm_xt_cols, workspace)
+from . import (MOE_ACT_NONE, MOE_ACT_SILU_MUL, MOE_BF16, MOE_E4M3FN, MOE_E8M0, MOE_F32, MOE_MX4, MOE_OP_BALANCE,
+               MOE_OP_FFN_TOKENS, MOE_OP_GATHER_REDUCE, MOE_OP_GMM, MOE_OP_GMM_B128, MOE_OP_GMM_MX4,
+               MOE_OP_QUANTIZE_ROWS, MOE_OP_SORT_BY_EXPERT, MOE_OP_TGMM, MOE_OP_TGMM_B128, MOE_SCALE_ROW_DYNAMIC,
+               MOE_SCALE_TENSOR_DYNAMIC, MOE_SCALE_TENSOR_FROM_ROW_AMAX, MOE_SCALE_TENSOR_STATIC, MOE_SCORE_SOFTMAX,
+               moe_balance_loss, moe_balance_loss_backward, moe_ffn_tokens, moe_gather_reduce,
+               moe_gather_reduce_backward, moe_gmm_b128, moe_gmm_fp8, moe_gmm_mx4, moe_quantize_cols_b128,
+               moe_quantize_rows, moe_quantize_rows_b128, moe_quantize_rows_mx4, moe_quantize_rows_strided,
+               moe_quantize_sort_by_expert, moe_quantize_weights, moe_quantize_weights_b128, moe_quantize_weights_mx4,
+               moe_router_topk, moe_router_topk_backward, moe_silu_mul_backward, moe_sort_by_expert,
+               moe_sort_gather_transposed, moe_tgmm_b128, moe_tgmm_fp8, moe_tgmm_fp8_xt, tgmm_xt_cols, workspace)
 
 
 def bf16_tensor(bits: np.ndarray, device) -> torch.Tensor:
@@ -721,6 +725,247 @@ class RoutedFFN:
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             self.step()
+        torch.cuda.synchronize()
+        self.graph = g
+        return g
+
+    def replay(self):
+        self.graph.replay()
+
+
+class B128Weight:
+    """An expert weight [E, K, N] bf16 in e4m3 with an e8m0 scale for every block
+    of 128 by 128: codes [E, N, K] for x W, and [E, K, N] for dy W^T."""
+
+    def __init__(self, w_bf16: torch.Tensor, stream=None):
+        self.E, self.K, self.N = w_bf16.shape
+        kb, nb, dev = -(-self.K // 128), -(-self.N // 128), w_bf16.device
+        self.q = torch.empty((self.E, self.N, self.K), dtype=torch.uint8, device=dev)
+        self.scale = torch.empty((self.E, kb, 1, nb), dtype=torch.uint8, device=dev)
+        self.qt = torch.empty((self.E, self.K, self.N), dtype=torch.uint8, device=dev)
+        self.scale_t = torch.empty((self.E, nb, 1, kb), dtype=torch.uint8, device=dev)
+        self.quantize(w_bf16, stream)
+
+    def quantize(self, w_bf16, stream=None):
+        """The weight's new values, as after an optimizer step."""
+        moe_quantize_weights_b128(w_bf16, self.E, self.K, self.N, self.q, self.scale, self.qt, self.scale_t, stream=stream)
+
+
+class B128Rows:
+    """Rows [R, C] in e4m3 with a scale for every block of 128, codes and scales
+    as parts of one row (of whole lines), so that one gather moves both."""
+
+    def __init__(self, R, C, device):
+        self.C, self.kb = C, -(-C // 128)
+        self.ld = -(-(C + self.kb) // 128) * 128
+        self.rows = torch.zeros((R, self.ld), dtype=torch.uint8, device=device)
+        self.q, self.scale = self.rows[:, :C], self.rows[:, C:C + self.kb]
+
+    def quantize(self, x, x_up, ldx, act, R):
+        moe_quantize_rows_b128(x, x_up, ldx, act, R, self.C, self.q, self.ld, self.scale, self.ld)
+
+
+class B128Cols:
+    """Rows [M, C] of the local groups, quantized along each group's rows: the
+    weight gradient's operand."""
+
+    def __init__(self, M, C, E, device):
+        cols = tgmm_xt_cols(M, E)
+        self.C = C
+        self.q = torch.empty((C, cols), dtype=torch.uint8, device=device)
+        self.scale = torch.empty((cols // 128, C), dtype=torch.uint8, device=device)
+
+
+class BlockScaledFFN:
+    """A training step of the gated expert layer of ``T`` tokens from the
+    router's logits [T, E], its products in e4m3 with a scale for every block
+    of 128 of both operands:
+
+      step()         router -> tokens to rows -> sort -> [a | b] = gmm ->
+                     SiLU*mul to rows -> gmm -> gather-reduce -> ``out``;
+                     with ``balance_weight`` also the balance loss of every
+                     sequence (``loss`` [S], ``counts`` [S, E], ``tokens`` [S])
+      backward(dout) the gradients ``dx`` [T, H] bf16, ``dw01`` [E_loc, H, 2I]
+                     and ``dwo`` [E_loc, I, H] (grad_dtype), and ``dlogits``
+                     [T, E]: through the routing weights, plus balance_weight
+                     times the mean of the sequences' losses
+
+    ``w0``, ``w1`` [E_loc, H, I] and ``wo`` [E_loc, I, H] bf16 are quantized
+    here and by requantize(); ``x`` [T, H] bf16 and ``logits`` [T, E] (bf16 or
+    f32) are the buffers a step reads.  seq_offsets [S + 1] int32: where the
+    packed sequences begin (None: one of T tokens)."""
+
+    def __init__(self, x, logits, w0, w1, wo, k, score=MOE_SCORE_SOFTMAX, renormalize=True, weight_scale=1.0,
+                 select_bias=None, group_offset=0, m_cap=None, balance_weight=0.0, seq_offsets=None, grad_dtype=torch.float32):
+        if x.dim() != 2 or logits.dim() != 2 or w0.dim() != 3:
+            raise ValueError("x and logits have two dimensions, the weights three")
+        dev = x.device
+        self.x, self.logits, self.k = x, logits, k
+        self.T, self.H = T, H = x.shape
+        self.E, self.El, self.g0, self.I = E, El, g0, I = logits.shape[1], w0.shape[0], group_offset, w0.shape[2]
+        # the library sees addresses: what a buffer holds, and how much, is checked here
+        f32, i32, bf = torch.float32, torch.int32, torch.bfloat16
+        _expect("x", x, (T, H), (bf,), dev)
+        _expect("logits", logits, (T, E), (bf, f32), dev)
+        _expect("w0", w0, (El, H, I), (bf,), dev, strided=True)
+        _expect("w1", w1, (El, H, I), (bf,), dev, strided=True)
+        _expect("wo", wo, (El, I, H), (bf,), dev)
+        if select_bias is not None:
+            _expect("select_bias", select_bias, (E,), (f32,), dev)
+        if seq_offsets is not None and (seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2):
+            raise ValueError("seq_offsets holds where each sequence begins, and the last one's end")
+        S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+        if seq_offsets is not None:
+            _expect("seq_offsets", seq_offsets, (S + 1,), (i32,), dev)
+        if not 1 <= k <= min(E, 64):
+            raise ValueError("k must lie between 1 and the number of experts, at most 64")
+        if group_offset < 0 or group_offset + El > E:
+            raise ValueError("the local experts must be among the logits' experts")
+        if m_cap is not None and m_cap < 0:
+            raise ValueError("m_cap must not be negative")
+        if H % 16 or I % 16:
+            raise ValueError("H and I must be multiples of 16")
+        if grad_dtype not in (bf, f32):
+            raise ValueError("grad_dtype must be torch.bfloat16 or torch.float32")
+        self.logits_dtype = MOE_BF16 if logits.dtype == bf else MOE_F32
+        self.routing = (score, int(renormalize), float(weight_scale))
+        self.bias, self.offsets, self.S, self.balance_weight = select_bias, seq_offsets, S, float(balance_weight)
+        self.w01 = B128Weight(torch.cat([w0, w1], dim=2).contiguous())
+        self.wo = B128Weight(wo)
+        M = T * k
+        self.m_cap = Mc = M if m_cap is None else m_cap
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
+        self.ids, self.topk_w, self.out = new((T, k), i32), new((T, k), f32), new((T, H), bf)
+        self.perm, self.inv_pos, self.group_sizes = new(M, i32), new(M, i32), new(E, i32)
+        self.xq, self.xs, self.hq = B128Rows(T, H, dev), B128Rows(Mc, H, dev), B128Rows(Mc, I, dev)
+        self.one = torch.ones((1,), dtype=f32, device=dev)
+        self.ab, self.y = new((Mc, 2 * I), bf), new((Mc, H), bf)
+        self.loss, self.counts, self.tokens = (torch.zeros(n, dtype=d, device=dev) for n, d in ((S, f32), ((S, E), i32), (S, i32)))
+        self.dloss = torch.full((S,), self.balance_weight / S, dtype=f32, device=dev)
+        self.ws_sort = workspace(MOE_OP_SORT_BY_EXPERT, M, 0, 0, E, device=dev)
+        self.ws_up = workspace(MOE_OP_GMM_B128, Mc, H, 2 * I, E, device=dev)
+        self.ws_down = workspace(MOE_OP_GMM_B128, Mc, I, H, E, device=dev)
+        self.ws_balance = workspace(MOE_OP_BALANCE, T, S, 0, E, device=dev)
+        # the backward pass
+        self.dy, self.dh, self.dab, self.dxs = (new((Mc, C), bf) for C in (H, I, 2 * I, H))
+        self.dw = new((T, k), f32)
+        self.dyq, self.dabq = B128Rows(Mc, H, dev), B128Rows(Mc, 2 * I, dev)
+        self.xt, self.ht, self.dyt, self.dabt = (B128Cols(Mc, C, E, dev) for C in (H, I, H, 2 * I))
+        self.dw01, self.dwo = new((El, H, 2 * I), grad_dtype), new((El, I, H), grad_dtype)
+        self.grad_dtype = MOE_BF16 if grad_dtype == bf else MOE_F32
+        self.dx, self.dlogits = new((T, H), bf), torch.empty_like(logits)
+        self.ones = torch.ones((T, k), dtype=f32, device=dev)
+        self.ws_dh = workspace(MOE_OP_GMM_B128, Mc, H, I, E, device=dev)
+        self.ws_dx = workspace(MOE_OP_GMM_B128, Mc, 2 * I, H, E, device=dev)
+        self.ws_dwo = workspace(MOE_OP_TGMM_B128, Mc, I, H, E, device=dev)
+        self.ws_dw01 = workspace(MOE_OP_TGMM_B128, Mc, H, 2 * I, E, device=dev)
+
+    def requantize(self, w0, w1, wo):
+        """New weights, as after an optimizer step."""
+        dev, bf = self.x.device, (torch.bfloat16,)
+        _expect("w0", w0, (self.El, self.H, self.I), bf, dev, strided=True)
+        _expect("w1", w1, (self.El, self.H, self.I), bf, dev, strided=True)
+        _expect("wo", wo, (self.El, self.I, self.H), bf, dev)
+        self.w01.quantize(torch.cat([w0, w1], dim=2).contiguous())
+        self.wo.quantize(wo)
+
+    # -- forward -------------------------------------------------------------
+    def _gmm(self, rows, w, transposed, out, ws):
+        q, scale, K, N = (w.qt, w.scale_t, w.N, w.K) if transposed else (w.q, w.scale, w.K, w.N)
+        moe_gmm_b128(rows.q, rows.ld, rows.scale, rows.ld, q, scale, MOE_E8M0, self.group_sizes, self.E, self.g0, self.El,
+                     self.m_cap, K, N, MOE_BF16, out, ws)
+
+    def route(self):
+        moe_router_topk(self.logits, self.logits_dtype, self.E, self.T, self.E, self.k, self.routing[0], self.bias,
+                        self.routing[1], self.routing[2], self.ids, self.topk_w)
+        if self.balance_weight:
+            moe_balance_loss(self.logits, self.logits_dtype, self.E, self.ids, self.T, self.E, self.k, self.routing[0],
+                             self.offsets, self.S, self.loss, self.counts, self.tokens, self.ws_balance)
+
+    def sort(self):
+        self.xq.quantize(self.x, None, self.H, MOE_ACT_NONE, self.T)
+        moe_sort_by_expert(self.ids, self.T, self.k, self.E, self.g0, self.El, self.xq.rows, self.one, MOE_SCALE_TENSOR_STATIC,
+                           self.xq.ld, self.m_cap, self.perm, self.inv_pos, self.group_sizes, self.xs.rows, None, self.ws_sort)
+
+    def experts(self):
+        I = self.I
+        self._gmm(self.xs, self.w01, False, self.ab, self.ws_up)
+        self.hq.quantize(self.ab[:, :I], self.ab[:, I:], 2 * I, MOE_ACT_SILU_MUL, self.m_cap)
+        self._gmm(self.hq, self.wo, False, self.y, self.ws_down)
+
+    def combine(self):
+        moe_gather_reduce(self.y, MOE_BF16, self.inv_pos, self.topk_w, self.T, self.k, self.H, MOE_BF16, self.out)
+
+    def step(self):
+        if self.T == 0:                # no tokens: no results; losses and counts stay zero
+            return
+        self.route()
+        self.sort()
+        self.experts()
+        self.combine()
+
+    # -- backward ------------------------------------------------------------
+    def _cols(self, to, x, x_up, ldx, act, T, k, perm, ws):
+        moe_quantize_cols_b128(x, x_up, ldx, act, T, k, perm, self.group_sizes, self.E, self.g0, self.El, self.m_cap, to.C, to.q,
+                               to.scale, ws)
+
+    def _tgmm(self, x, y, out, ws):
+        moe_tgmm_b128(x.q, x.scale, y.q, y.scale, self.group_sizes, self.E, self.g0, self.El, self.m_cap, x.C, y.C,
+                      self.grad_dtype, out, ws)
+
+    def combine_backward(self, dout):
+        moe_gather_reduce_backward(dout, self.y, self.inv_pos, self.topk_w, self.T, self.k, self.H, self.group_sizes, self.E,
+                                   self.g0, self.El, self.m_cap, self.dy, self.dw)
+
+    def router_backward(self):
+        moe_router_topk_backward(self.logits, self.logits_dtype, self.E, self.ids, self.dw, self.T, self.E, self.k,
+                                 self.routing[0], self.routing[1], self.routing[2], self.dlogits, self.E)
+        if self.balance_weight:
+            moe_balance_loss_backward(self.logits, self.logits_dtype, self.E, self.counts, self.tokens, self.dloss, self.T, self.E,
+                                      self.k, self.routing[0], self.offsets, self.S, 1, self.dlogits, self.E)
+
+    def down_backward(self):
+        I, Mc = self.I, self.m_cap
+        self.dyq.quantize(self.dy, None, self.H, MOE_ACT_NONE, Mc)
+        self._gmm(self.dyq, self.wo, True, self.dh, self.ws_dh)
+        self._cols(self.ht, self.ab[:, :I], self.ab[:, I:], 2 * I, MOE_ACT_SILU_MUL, Mc, 1, None, self.ws_dwo)
+        self._cols(self.dyt, self.dy, None, self.H, MOE_ACT_NONE, Mc, 1, None, self.ws_dwo)
+        self._tgmm(self.ht, self.dyt, self.dwo, self.ws_dwo)
+
+    def up_backward(self):
+        I, Mc = self.I, self.m_cap
+        moe_silu_mul_backward(self.ab[:, :I], self.ab[:, I:], 2 * I, self.dh, Mc, I, self.dab[:, :I], self.dab[:, I:], 2 * I)
+        self.dabq.quantize(self.dab, None, 2 * I, MOE_ACT_NONE, Mc)
+        self._gmm(self.dabq, self.w01, True, self.dxs, self.ws_dx)
+        moe_gather_reduce(self.dxs, MOE_BF16, self.inv_pos, self.ones, self.T, self.k, self.H, MOE_BF16, self.dx)
+        self._cols(self.xt, self.x, None, self.H, MOE_ACT_NONE, self.T, self.k, self.perm, self.ws_dw01)
+        self._cols(self.dabt, self.dab, None, 2 * I, MOE_ACT_NONE, Mc, 1, None, self.ws_dw01)
+        self._tgmm(self.xt, self.dabt, self.dw01, self.ws_dw01)
+
+    def backward(self, dout):
+        """dout [T, H] bf16, the gradient of ``out``, after a step."""
+        _expect("dout", dout, (self.T, self.H), (torch.bfloat16,), self.x.device)
+        if self.T == 0:
+            self.dw01.zero_()
+            self.dwo.zero_()
+            return
+        self.combine_backward(dout)
+        self.router_backward()
+        self.down_backward()
+        self.up_backward()
+
+    # -- HIP graph of one step and its backward pass ---------------------------
+    def capture_graph(self, dout, warmup=2):
+        """Record a step and its backward pass into a HIP graph (every buffer
+        they write is fully rewritten, so replays equal eager steps)."""
+        for _ in range(warmup):
+            self.step()
+            self.backward(dout)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            self.step()
+            self.backward(dout)
         torch.cuda.synchronize()
         self.graph = g
         return g
