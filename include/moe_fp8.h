@@ -801,7 +801,7 @@ int moe_quantize_cols_b128(const void* x, const void* x_up, int64_t ldx, int act
  *            group (E = 1, its size M) is a plain linear layer.
  *   ws       workspace of moe_workspace_bytes(MOE_OP_GMM_B128, M, K, N, E).
  * K and N multiples of 16 and at most 2^22, N * ceil(K/128) < 2^31; ldl a multiple
- * of 16, K to 2^23; lds a multiple of 16, at least ceil(K/128); lhs,
+ * of 16, K to 2^22; lds a multiple of 16, at least ceil(K/128); lhs,
  * lhs_scale, rhs, out 16-byte aligned.  Errors as in moe_gmm_fp8.
  */
 int moe_gmm_b128(const uint8_t* lhs, int64_t ldl, const uint8_t* lhs_scale, int64_t lds, const uint8_t* rhs,

@@ -874,8 +874,9 @@ extern "C" int moe_gmm_b128(const uint8_t* lhs, int64_t ldl, const uint8_t* lhs_
   if (E <= 0 || E > 1024 || group_offset < 0 || num_local_experts < 0 || num_local_experts > kMaxLocal ||
       group_offset > E - num_local_experts)
     return MOE_ERR_SHAPE;
-  // row offsets inside a tile, and a group's weights' scales, are 32-bit
-  if (M > INT32_MAX - 1 || K > (1 << 22) || ldl > (1 << 23) || N > (1 << 22) || N * moe_cdiv(K, 128) > INT32_MAX) return MOE_ERR_SHAPE;
+  // row offsets inside a tile, and a group's weights' scales, are 32-bit; a tile's rows span less than 2^31 bytes, so that
+  // chunks past K, at 2^31, lie outside its buffer
+  if (M > INT32_MAX - 1 || K > (1 << 22) || ldl > (1 << 22) || N > (1 << 22) || N * moe_cdiv(K, 128) > INT32_MAX) return MOE_ERR_SHAPE;
   // the tile table of any split of M rows into the groups stays below 2^31 entries
   if ((moe_cdiv(M, 16) + num_local_experts + 1) * (N / 16) > INT32_MAX) return MOE_ERR_SHAPE;
   if (ldl < K || ldl % 16 || lds < moe_cdiv(K, 128) || lds % 16 || lds > (1 << 23)) return MOE_ERR_SHAPE;

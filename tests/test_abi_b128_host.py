@@ -63,7 +63,7 @@ def test_gmm(lib):
           wsb=1 << 40):
         return lib.moe_gmm_b128(lhs, ldl, ls, lds, rhs, rs, sdt, gs, E, g0, El, M, K, N, dt, out, ws, wsb, None)
     check(f, [dict(K=136), dict(N=24), dict(K=0), dict(N=0), dict(M=-1), dict(M=2 ** 31), dict(M=BIG), dict(K=(1 << 22) + 16, ldl=1 << 23, lds=1 << 16),
-              dict(N=BIG), dict(E=0), dict(E=2000), dict(g0=4, El=5), dict(ldl=128), dict(ldl=152), dict(ldl=(1 << 23) + 16), dict(lds=0), dict(lds=8),
+              dict(N=BIG), dict(E=0), dict(E=2000), dict(g0=4, El=5), dict(ldl=128), dict(ldl=152), dict(ldl=(1 << 23) + 16), dict(ldl=(1 << 22) + 16), dict(lds=0), dict(lds=8),
               dict(K=2064, ldl=2064), dict(lds=(1 << 23) + 16), dict(lhs=AL + 8), dict(ls=AL + 8), dict(rhs=AL + 8), dict(out=AL + 8),
               dict(sdt=m.MOE_F32, rs=AL + 2), dict(M=2 ** 31 - 2, N=1 << 14)],
           [dict(sdt=m.MOE_BF16), dict(sdt=9), dict(dt=5)],
