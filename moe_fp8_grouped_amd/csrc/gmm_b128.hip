@@ -499,7 +499,7 @@ __device__ __forceinline__ void run_wide(const B128Args& p, WideLds<KIND>& sm, S
 }
 
 // Persistent workgroups, one a CU.  A group's rows are spread evenly over as few tiles as hold them; the tile range is
-// split over the XCDs, row tiles fastest, so that a group's weights are fetched once and shared in L2.
+// split over the XCDs, row tiles (tgmm: column tiles) fastest, so that a group's weights are fetched once and shared in L2.
 template <Kind KIND, bool OUT_BF16>
 __global__ __launch_bounds__(kWideThreads, 2) void b128_wide_kernel(const B128Args p) {
   __shared__ __attribute__((aligned(1024))) WideLds<KIND> sm;
@@ -543,7 +543,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_wide_kernel(const B128Ar
     if (tid < count) {
       const int t = first + (base + tid) * step;
       if (TG) {
-        const int g = t / (RT * NT), l = t - g * RT * NT, ct = l / RT, rt = l - ct * RT;
+        const int g = t / (RT * NT), l = t - g * RT * NT, rt = l / NT, ct = l - rt * NT;
         sm.desc[tid] = make_int4(ROWS * rt, ct, g, min(ROWS, static_cast<int>(p.K) - ROWS * rt));
         sm.more[tid] = make_int2(gt.blocks_off[g + 1] - gt.blocks_off[g], gt.blocks_off[g]);
       } else {
