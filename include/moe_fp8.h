@@ -755,17 +755,16 @@ int moe_quantize_weights_b128(const void* w, int64_t E, int64_t K, int64_t N, ui
 
 /*
  * moe_quantize_cols_b128 -- the rows of each local group to e4m3fn with a
- * scale for every 128 of its rows and column, laid out column by column: the
- * operand of the weight gradient, whose contraction runs along a group's
- * rows.  With the local groups' sorted rows rows_off[g] .. rows_off[g] + m_g - 1
+ * scale for every 128 of its rows and column, every 128 rows laid out column
+ * by column: the operand of the weight gradient, whose contraction runs along
+ * a group's rows.  With the local groups' sorted rows rows_off[g] .. rows_off[g] + m_g - 1
  * and padded starts P_g = 128 * sum_{h<g} ceil(m_h / 128), as in
  * moe_sort_gather_transposed:
- *   qt[c, P_g + i]            code of V[rows_off[g] + i, c]   (i < m_g)
- *                             0            (m_g <= i < 128 * ceil(m_g / 128))
- *   scale_t[P_g / 128 + b, c] scale of rows 128 b .. of group g, column c
+ *   qt[(P_g + i) / 128, c, i % 128]  code of V[rows_off[g] + i, c]   (i < m_g)
+ *                                    0      (m_g <= i < 128 * ceil(m_g / 128))
+ *   scale_t[P_g / 128 + b, c]        scale of rows 128 b .. of group g, column c
  * scales and codes formed as in moe_quantize_rows_b128 along those rows.
- * Columns (of qt) and rows (of scale_t) past the last group's padded end are
- * not written.
+ * What lies past the last group's padded end, in both, is not written.
  *   V        the local sorted rows: with perm NULL, x itself, [M, C]; with
  *            perm [T*k] (moe_sort_by_expert's), V[r] = x[perm[start + r] / k],
  *            x [T, C] the tokens, start = sum of group_sizes[0 .. group_offset-1].
@@ -773,8 +772,8 @@ int moe_quantize_weights_b128(const void* w, int64_t E, int64_t K, int64_t N, ui
  *            (k is 1 to 64); without perm T is x's row count, at least M.
  *   group_sizes, E, group_offset, num_local_experts: as in the sort.
  *   M        local rows (rows of the weight gradient's operands).
- *   qt       [C, moe_tgmm_xt_cols(M, E)] bytes, scale_t [cols / 128, C] bytes,
- *            both 16-byte aligned.
+ *   qt       [cols / 128, C, 128] bytes, scale_t [cols / 128, C] bytes, cols =
+ *            moe_tgmm_xt_cols(M, E); both 16-byte aligned.
  *   ws       workspace of at least 256 bytes (the error word: negative sizes,
  *            more local rows than M; a row index outside x is clamped).
  * C a multiple of 16, M + 128 E <= 2^23.  Errors: MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED,
@@ -812,11 +811,11 @@ int moe_gmm_b128(const uint8_t* lhs, int64_t ldl, const uint8_t* lhs_scale, int6
 /*
  * moe_tgmm_b128 -- the weight gradient of moe_gmm_b128, both operands
  * quantized along the rows of each group (moe_quantize_cols_b128):
- *   out[g, k, c] = sum_b sx[b, k] * sy[b, c] * sum_{r in block b of group g} lhs_t[k, r] * rhs_t[c, r]
- * accumulated in float32 by the scaled matrix cores; an empty local group
- * gives zeros.
- *   lhs_t    [K, cols] codes, lhs_scale [cols / 128, K]; rhs_t [N, cols],
- *            rhs_scale [cols / 128, N]; cols = moe_tgmm_xt_cols(M, E).
+ *   out[g, k, c] = sum_b sx[b, k] * sy[b, c] * sum_{i < 128} lhs_t[b, k, i] * rhs_t[b, c, i]
+ * over the blocks b of group g, accumulated in float32 by the scaled matrix
+ * cores; an empty local group gives zeros.
+ *   lhs_t    [cols / 128, K, 128] codes, lhs_scale [cols / 128, K]; rhs_t
+ *            [cols / 128, N, 128], rhs_scale [cols / 128, N]; cols = moe_tgmm_xt_cols(M, E).
  *   group_sizes .. num_local_experts, M: as the operands were made with.
  *   out      [E_loc, K, N], out_dtype MOE_F32 (default) or MOE_BF16.
  *   ws       workspace of moe_workspace_bytes(MOE_OP_TGMM_B128, M, K, N, E).

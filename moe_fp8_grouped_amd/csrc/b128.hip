@@ -178,7 +178,7 @@ struct ColsArgs {
   const int32_t* perm;
   const int32_t* sizes;
   int g0, El;
-  int64_t M, C, cols;
+  int64_t M, C;
   uint8_t* qt;
   uint8_t* scale;
   int32_t* err;
@@ -187,7 +187,7 @@ struct ColsArgs {
 // A workgroup takes 128 rows of one group and every gridDim.y-th 128 of the
 // columns, the next ones' loads issued before these are worked on.  A thread
 // holds eight rows of eight columns; a column's maximum goes through LDS, and so
-// do its codes, which leave as one line of 128 bytes.
+// do its codes, which leave as lines of 128 bytes, one run for all columns.
 template <bool SILU>
 __global__ __launch_bounds__(256) void quantize_cols_b128_kernel(const ColsArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t codes[kBlock * kPitch];
@@ -267,7 +267,7 @@ __global__ __launch_bounds__(256) void quantize_cols_b128_kernel(const ColsArgs 
     for (int i = 0; i < 4; ++i) {
       const int col = (tid >> 3) + 32 * i;
       if (c0 + col < p.C)
-        *reinterpret_cast<uint4*>(p.qt + (c0 + col) * p.cols + static_cast<int64_t>(blk) * kBlock + 16 * (tid & 7)) =
+        *reinterpret_cast<uint4*>(p.qt + (blk * p.C + c0 + col) * kBlock + 16 * (tid & 7)) =
             *reinterpret_cast<const uint4*>(codes + col * kPitch + 16 * (tid & 7));
     }
     // (the next columns' maxima touch `tops` alone until their first barrier, behind these reads)
@@ -332,10 +332,8 @@ extern "C" int moe_quantize_cols_b128(const void* x, const void* x_up, int64_t l
   if (!x || !group_sizes || !qt || !scale_t || (act == MOE_ACT_SILU_MUL && !x_up)) return MOE_ERR_NULL;
   if (!moe::aligned(x, 16) || !moe::aligned(x_up, 16) || !moe::aligned(qt, 16) || !moe::aligned(scale_t, 16)) return MOE_ERR_SHAPE;
   if (!ws || ws_bytes < 256) return MOE_ERR_WORKSPACE;
-  int64_t cols = 0;
-  if (moe_tgmm_xt_cols(M, E, &cols) != MOE_OK) return MOE_ERR_SHAPE;
   const moe::ColsArgs p{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(x_up), ldx, T, k, perm, group_sizes,
-                        group_offset, num_local_experts, M, C, cols, qt, scale_t, static_cast<int32_t*>(ws)};
+                        group_offset, num_local_experts, M, C, qt, scale_t, static_cast<int32_t*>(ws)};
   // as many blocks as any split of M rows into the groups has
   const int64_t groups = num_local_experts < M ? num_local_experts : M;
   const int64_t blocks = moe_cdiv(M, 128) + groups, tiles = moe_cdiv(C, 128);

@@ -2,7 +2,7 @@
 // scale over every 128 elements of the contraction, on the gfx950 scaled matrix
 // cores (v_mfma_scale_f32_16x16x128_f8f6f4, float32 accumulate):
 //   gmm    out[r, c] = sum_b sx[r, b] sw[g, b, c / 128] sum_{k in b} X[r, k] W_g[c, k]
-//   tgmm   out[g, k, c] = sum_b sx[b, k] sy[b, c] sum_{r in b} Xt[k, r] Yt[c, r]
+//   tgmm   out[g, k, c] = sum_b sx[b, k] sy[b, c] sum_{r in b} Xt[b, k, r] Yt[b, c, r]
 // One matrix instruction spans one block of the contraction, and its e8m0
 // operands apply both scales: they cost nothing.
 //
@@ -24,11 +24,11 @@ using namespace stage;
 enum Kind { kGmmE8M0, kGmmF32, kTgmm };
 
 struct B128Args {
-  const uint8_t* x;            // gmm: rows [M, K]; tgmm: [K, cols]
+  const uint8_t* x;            // gmm: rows [M, K]; tgmm: [cols / 128, K, 128]
   int64_t ldx;
   const uint8_t* xs;           // gmm: [M, lds]; tgmm: [cols / 128, K]
   int64_t lds;
-  const uint8_t* w;            // gmm: [El, N, K]; tgmm: [N, cols]
+  const uint8_t* w;            // gmm: [El, N, K]; tgmm: [cols / 128, N, 128]
   const void* ws;              // gmm: [El, kb, nb]; tgmm: [cols / 128, N]
   const int32_t* sizes;
   int g0, El;
@@ -247,7 +247,8 @@ __device__ __forceinline__ WideTile wide_tile(const LDS& sm, int i) {
 // One operand's loads: where they are in the stream of tiles and stages, and to which buffer the next goes.
 template <Kind KIND, bool OUT_BF16, bool ROWS>
 struct Cursor {
-  __amdgpu_buffer_rsrc_t buf;
+  __amdgpu_buffer_rsrc_t buf;                      // gmm: the tile's
+  const uint8_t* src;                              // tgmm: the stage's, which is one run of bytes
   WideTile t;
   int i, s, b;                                     // tile, stage, buffer
   bool more;                                       // whether there is such a stage
@@ -261,13 +262,10 @@ struct Cursor {
     }
     more = i < count;
     if (!more) return;
-    const uint32_t cols = static_cast<uint32_t>(min(static_cast<int>(p.N) - t.col0, kWideCols));
     if constexpr (KIND == kTgmm) {
-      const uint32_t len = 128u * t.steps, ld = static_cast<uint32_t>(p.ldx);
-      const int64_t at = 128 * static_cast<int64_t>(t.blk0);
-      buf = ROWS ? buffer(p.x + static_cast<int64_t>(t.row0) * p.ldx + at, (t.rows - 1) * ld + len) : buffer(p.w + static_cast<int64_t>(t.col0) * p.ldx + at, (cols - 1) * ld + len);
+      src = ROWS ? p.x + 128 * (t.blk0 * p.K + t.row0) : p.w + 128 * (t.blk0 * p.N + t.col0);
     } else {
-      const uint32_t K = static_cast<uint32_t>(p.K);
+      const uint32_t K = static_cast<uint32_t>(p.K), cols = static_cast<uint32_t>(min(static_cast<int>(p.N) - t.col0, kWideCols));
       buf = ROWS ? buffer(p.x + static_cast<int64_t>(t.row0) * p.ldx, (t.rows - 1) * static_cast<uint32_t>(p.ldx) + K)
                  : buffer(p.w + (static_cast<int64_t>(t.g) * p.N + t.col0) * p.K, cols * K);
     }
@@ -277,7 +275,12 @@ struct Cursor {
   // chunks past K lie outside the buffer: zeros.  (Weights are four loads always: the waits count them.)
   __device__ __forceinline__ void load(const B128Args& p, WideLds<KIND>& sm, int count, int wave, int lane) {
     const int r = 8 * wave + (lane >> 3);
-    const uint32_t ld = static_cast<uint32_t>(ROWS || KIND == kTgmm ? p.ldx : p.K);
+    const uint32_t ld = KIND == kTgmm ? 128u : static_cast<uint32_t>(ROWS ? p.ldx : p.K);
+    if constexpr (KIND == kTgmm) {
+      buf = buffer(src, 128u * static_cast<uint32_t>(ROWS ? t.rows : min(static_cast<int>(p.N) - t.col0, kWideCols)));
+      src += 128 * (ROWS ? p.K : p.N);
+    }
+    const uint32_t stage_at = KIND == kTgmm ? 0u : 128u * s;
     const uint32_t c = 16 * ((lane & 7) ^ (ROWS || !OUT_BF16 ? swz_run(r) : swz_quads(r)));
     // (64 places further on: tgmm 4 rows, and then the wave's other 128)
     uint32_t off = (ROWS ? row_at<KIND>(r) : r) * ld + c;
@@ -286,7 +289,7 @@ struct Cursor {
 #pragma unroll
     for (int j = 0; j < (ROWS ? kWideRows<KIND> : kWideCols) / 64; ++j)
       if (!ROWS || KIND == kTgmm || 64 * j + 8 * wave < t.rows)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void*)(dst + 64 * 128 * j), 16, off, 128u * s + (ROWS ? row_at<KIND>(64 * j) : 64 * j) * ld, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void*)(dst + 64 * 128 * j), 16, off, stage_at + (ROWS ? row_at<KIND>(64 * j) : 64 * j) * ld, 0, 0);
     b ^= 1;
     if (++s == t.steps) {
       ++i;
@@ -684,6 +687,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_narrow_kernel(const B128
     WideTile lt{};
     int li = 0, ls = 0, lb = 0, issued = 0;
     __amdgpu_buffer_rsrc_t xbuf = buffer(p.x, 0), wbuf = xbuf, xsbuf = xbuf, wsbuf = xbuf;
+    const uint8_t *xsrc = nullptr, *wsrc = nullptr;
     uint32_t odd = 0;
     auto seek = [&] {
       ls = 0;
@@ -692,14 +696,12 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_narrow_kernel(const B128
         if (lt.steps > 0) break;
       }
       if (li >= count) return;
-      const uint32_t cols = static_cast<uint32_t>(min(static_cast<int>(p.N) - lt.col0, kNarrow));
       if constexpr (TG) {
-        const uint32_t len = 128u * lt.steps, ld = static_cast<uint32_t>(p.ldx);
-        const int64_t at = 128 * static_cast<int64_t>(lt.blk0);
-        xbuf = buffer(p.x + static_cast<int64_t>(lt.row0) * p.ldx + at, (lt.rows - 1) * ld + len);
-        wbuf = buffer(p.w + static_cast<int64_t>(lt.col0) * p.ldx + at, (cols - 1) * ld + len);
+        xsrc = p.x + 128 * (lt.blk0 * p.K + lt.row0);
+        wsrc = p.w + 128 * (lt.blk0 * p.N + lt.col0);
       } else {
         const uint32_t K = static_cast<uint32_t>(p.K), lds = static_cast<uint32_t>(p.lds);
+        const uint32_t cols = static_cast<uint32_t>(min(static_cast<int>(p.N) - lt.col0, kNarrow));
         xbuf = buffer(p.x + static_cast<int64_t>(lt.row0) * p.ldx, (lt.rows - 1) * static_cast<uint32_t>(p.ldx) + K);
         wbuf = buffer(p.w + (static_cast<int64_t>(lt.g) * p.N + lt.col0) * p.K, cols * K);
         xsbuf = buffer(p.xs + lt.row0 * p.lds, lt.rows * lds);
@@ -710,7 +712,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_narrow_kernel(const B128
       }
     };
     const int lr = 8 * wave + (lane >> 3);         // the staged row that the lane fills
-    const uint32_t ldx = static_cast<uint32_t>(p.ldx), ldw = static_cast<uint32_t>(TG ? p.ldx : p.K);
+    const uint32_t ldx = TG ? 128u : static_cast<uint32_t>(p.ldx), ldw = TG ? 128u : static_cast<uint32_t>(p.K);
     const uint32_t xc = 16 * ((lane & 7) ^ swz_run(lr)), wch = 16 * ((lane & 7) ^ (OUT_BF16 ? swz_quads(lr) : swz_run(lr)));
     // one load of each operand a wave; waves 0 and 1 bring the scales as well
     auto load = [&] {
@@ -719,6 +721,13 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_narrow_kernel(const B128
         const uint32_t end = static_cast<uint32_t>(p.K) - 128u * ls;
         xo = xc < end ? xo : 0x80000000u;
         wo = wch < end ? wo : 0x80000000u;
+      }
+      const uint32_t at = TG ? 0u : 128u * ls;
+      if constexpr (TG) {
+        xbuf = buffer(xsrc, 128u * lt.rows);
+        wbuf = buffer(wsrc, 128u * static_cast<uint32_t>(min(static_cast<int>(p.N) - lt.col0, kNarrow)));
+        xsrc += 128 * p.K;
+        wsrc += 128 * p.N;
       }
       if (wave == 0) {
         if constexpr (TG) {
@@ -733,12 +742,12 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_narrow_kernel(const B128
                                                   static_cast<uint32_t>(min(static_cast<int>(p.N) - lt.col0, kNarrow)));
           __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)sm.ws[lb], 4, 4 * lane, 0, 0, 0);
         } else {
-          const uint32_t at = KIND == kGmmF32 ? 4u * ls * nb : (odd + ls * nb) & ~3u;
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(wsbuf, (lds_void*)sm.ws[lb], 4, at, 0, 0, 0);
+          const uint32_t scale_at = KIND == kGmmF32 ? 4u * ls * nb : (odd + ls * nb) & ~3u;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(wsbuf, (lds_void*)sm.ws[lb], 4, scale_at, 0, 0, 0);
         }
       }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wbuf, (lds_void*)(sm.w[lb] + 1024 * wave), 16, wo, 128u * ls, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xbuf, (lds_void*)(sm.x[lb] + 1024 * wave), 16, xo, 128u * ls, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wbuf, (lds_void*)(sm.w[lb] + 1024 * wave), 16, wo, at, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xbuf, (lds_void*)(sm.x[lb] + 1024 * wave), 16, xo, at, 0, 0);
       order();
       lb = lb + 1 == NST ? 0 : lb + 1;
       ++issued;
@@ -911,7 +920,7 @@ extern "C" int moe_tgmm_b128(const uint8_t* lhs_t, const uint8_t* lhs_scale, con
       group_offset > E - num_local_experts)
     return MOE_ERR_SHAPE;
   if (M > (int64_t{1} << 23) || M + 128 * static_cast<int64_t>(E) > (int64_t{1} << 23)) return MOE_ERR_SHAPE;
-  // tiles are counted in 32 bits, a tile's rows span less than 2^32 bytes
+  // tiles are counted in 32 bits
   if (moe_cdiv(K, 16) * moe_cdiv(N, 16) > INT32_MAX / (num_local_experts > 0 ? num_local_experts : 1)) return MOE_ERR_SHAPE;
   if (out_dtype == MOE_DTYPE_DEFAULT) out_dtype = MOE_F32;
   if (out_dtype != MOE_BF16 && out_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
@@ -923,9 +932,7 @@ extern "C" int moe_tgmm_b128(const uint8_t* lhs_t, const uint8_t* lhs_scale, con
     return MOE_ERR_SHAPE;
   if (!ws || ws_bytes < moe::tgmm_b128_ws_bytes()) return MOE_ERR_WORKSPACE;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  int64_t cols = 0;
-  if (moe_tgmm_xt_cols(M, E, &cols) != MOE_OK) return MOE_ERR_SHAPE;
-  const moe::B128Args p{lhs_t, cols, lhs_scale, 0, rhs_t, rhs_scale, group_sizes, group_offset, num_local_experts, M, K, N, out,
+  const moe::B128Args p{lhs_t, 0, lhs_scale, 0, rhs_t, rhs_scale, group_sizes, group_offset, num_local_experts, M, K, N, out,
                         static_cast<int32_t*>(ws)};
   const hipError_t e = out_dtype == MOE_BF16 ? moe::launch_b128<moe::kTgmm, true>(p, st) : moe::launch_b128<moe::kTgmm, false>(p, st);
   return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;

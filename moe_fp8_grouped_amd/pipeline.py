@@ -772,7 +772,7 @@ class B128Cols:
     def __init__(self, M, C, E, device):
         cols = tgmm_xt_cols(M, E)
         self.C = C
-        self.q = torch.empty((C, cols), dtype=torch.uint8, device=device)
+        self.q = torch.empty((cols // 128, C, 128), dtype=torch.uint8, device=device)
         self.scale = torch.empty((cols // 128, C), dtype=torch.uint8, device=device)
 
 

@@ -102,6 +102,18 @@ def quantize_cols_b128(v, group_sizes, g0, El, M, cols):
     return qt, st, written
 
 
+def blocks_of(qt):
+    """Codes [C, cols] as the calls lay them out: [cols / 128, C, 128]."""
+    C, cols = qt.shape
+    return np.ascontiguousarray(qt.reshape(C, cols // BLOCK, BLOCK).transpose(1, 0, 2))
+
+
+def columns_of(blocks):
+    """The way back."""
+    n, C, _ = blocks.shape
+    return np.ascontiguousarray(blocks.transpose(1, 0, 2)).reshape(C, n * BLOCK)
+
+
 def spread(s, n):
     """Block scales [..., blocks] over n elements of the last axis."""
     return np.repeat(s, BLOCK, axis=-1)[..., :n]

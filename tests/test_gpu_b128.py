@@ -158,7 +158,7 @@ def test_columns_bit_exact(case):
     wide = [torch.full((T, ldx), 1e30, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
     for t, b in zip(wide, (xb, xu)):
         t[:, 8:8 + C] = dev_bf16(b)
-    qt = torch.full((C, cols), 0xAA, dtype=torch.uint8, device="cuda")
+    qt = torch.full((cols // 128, C, 128), 0xAA, dtype=torch.uint8, device="cuda")
     st = torch.full((cols // 128, C), 0xAA, dtype=torch.uint8, device="cuda")
     ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
     m.moe_quantize_cols_b128(wide[0][:, 8:8 + C], wide[1][:, 8:8 + C] if gated else None, ldx, m.MOE_ACT_SILU_MUL if gated else m.MOE_ACT_NONE,
@@ -166,7 +166,7 @@ def test_columns_bit_exact(case):
     with np.errstate(all="ignore"):
         v = b128.values(xb[src], xu[src] if gated else None)
     oq, os_, written = b128.quantize_cols_b128(v, gs, g0, El, M, cols)
-    q, s = host(qt), host(st)
+    q, s = b128.columns_of(host(qt)), host(st)
     assert_bits_equal(s[written[::128]], os_[written[::128]], "scales")
     assert_bits_equal(q[:, written], oq[:, written], "codes")
     assert (q[:, ~written] == 0xAA).all() and (s[~written[::128]] == 0xAA).all()
@@ -179,7 +179,7 @@ def test_columns_of_bad_sizes_and_indexes_stay_inside():
     x = dev_bf16(bits(rng, T, C))
     cols = m.tgmm_xt_cols(M, E)
     for gs, bit in (([50, -3, 30, 0], m.MOE_DEVERR_GROUP_SIZE), ([50, 60, 2 ** 31 - 1, 2 ** 31 - 1], m.MOE_DEVERR_ROWS)):
-        qt = torch.zeros((C, cols), dtype=torch.uint8, device="cuda")
+        qt = torch.zeros((cols // 128, C, 128), dtype=torch.uint8, device="cuda")
         st = torch.zeros((cols // 128, C), dtype=torch.uint8, device="cuda")
         ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
         perm = rng.integers(-2 ** 31, 2 ** 31, T * k).astype(np.int32)
@@ -322,7 +322,7 @@ def test_product_names_bad_sizes_and_stays_inside():
         assert m.moe_debug_check(work) == bit
         dw, work = torch.zeros((E, K, N), device="cuda"), m.workspace(m.MOE_OP_TGMM_B128, M, K, N, E)
         cols = m.tgmm_xt_cols(M, E)
-        t = [torch.full((c, cols), 0x38, dtype=torch.uint8, device="cuda") for c in (K, N)]
+        t = [torch.full((cols // 128, c, 128), 0x38, dtype=torch.uint8, device="cuda") for c in (K, N)]
         s = [torch.full((cols // 128, c), 120, dtype=torch.uint8, device="cuda") for c in (K, N)]
         m.moe_tgmm_b128(t[0], s[0], t[1], s[1], dev_i32(gs), E, 0, E, M, K, N, m.MOE_F32, dw, work)
         assert m.moe_debug_check(work) == bit
@@ -361,7 +361,7 @@ def test_weight_gradient(case, dtype):
         q.append(a), s.append(b)
     out = torch.full((El, K, N), float("nan"), dtype=torch.bfloat16 if dtype == m.MOE_BF16 else torch.float32, device="cuda")
     work = m.workspace(m.MOE_OP_TGMM_B128, M, K, N, E)
-    m.moe_tgmm_b128(dev_u8(q[0]), dev_u8(s[0]), dev_u8(q[1]), dev_u8(s[1]), dev_i32(gs), E, g0, El, M, K, N, dtype, out, work)
+    m.moe_tgmm_b128(dev_u8(b128.blocks_of(q[0])), dev_u8(s[0]), dev_u8(b128.blocks_of(q[1])), dev_u8(s[1]), dev_i32(gs), E, g0, El, M, K, N, dtype, out, work)
     got = read(out)
     o, A = b128.tgmm_b128(q[0], s[0], q[1], s[1], gs, g0, El, M)
     p = 0
@@ -404,7 +404,7 @@ def test_the_same_bits_every_time_and_in_a_graph(M, El):
     kb, nb, cols = -(-K // 128), -(-N // 128), m.tgmm_xt_cols(M, El)
     u8 = dict(dtype=torch.uint8, device="cuda")
     b = dict(q=torch.zeros(M, K + 16, **u8), wq=torch.zeros(El, N, K, **u8), ws=torch.zeros(El, kb, 1, nb, **u8), wt=torch.zeros(El, K, N, **u8),
-             wst=torch.zeros(El, nb, 1, kb, **u8), xt=torch.zeros(K, cols, **u8), xts=torch.zeros(cols // 128, K, **u8), yt=torch.zeros(N, cols, **u8),
+             wst=torch.zeros(El, nb, 1, kb, **u8), xt=torch.zeros(cols // 128, K, 128, **u8), xts=torch.zeros(cols // 128, K, **u8), yt=torch.zeros(cols // 128, N, 128, **u8),
              yts=torch.zeros(cols // 128, N, **u8), y=torch.zeros(M, N, dtype=torch.bfloat16, device="cuda"), dw=torch.zeros(El, K, N, device="cuda"))
     work, twork = m.workspace(m.MOE_OP_GMM_B128, M, K, N, El), m.workspace(m.MOE_OP_TGMM_B128, M, K, N, El)
     x = torch.empty_like(xb)

@@ -44,8 +44,8 @@ def quantizers(o, s):
 
 def products(o, s):
     x, xs, w, ws = u8(0, 0x7F, T, H), u8(118, 122, T, 16), u8(0, 0x7F, E, I, H), u8(118, 122, E, H // 128, 1, I // 128)
-    cols = m.tgmm_xt_cols(T, E)
-    xt, xts, yt, yts = u8(0, 0x7F, H, cols), u8(118, 122, cols // 128, H), u8(0, 0x7F, I, cols), u8(118, 122, cols // 128, I)
+    n = m.tgmm_xt_cols(T, E) // 128
+    xt, xts, yt, yts = u8(0, 0x7F, n, H, 128), u8(118, 122, n, H), u8(0, 0x7F, n, I, 128), u8(118, 122, n, I)
     g, a, b = sizes(), m.workspace(m.MOE_OP_GMM_B128, T, H, I, E), m.workspace(m.MOE_OP_TGMM_B128, T, H, I, E)
 
     def call():
@@ -79,7 +79,7 @@ def ints(*shape):
 
 SETS = {
     "quantizers": (quantizers, lambda: dict(q=bytes_(T, H), s=bytes_(T, H // 128), wq=bytes_(E, I, H), ws=bytes_(E, H // 128, 1, I // 128),
-                                            wqt=bytes_(E, H, I), wst=bytes_(E, I // 128, 1, H // 128), ct=bytes_(H, m.tgmm_xt_cols(T, E)),
+                                            wqt=bytes_(E, H, I), wst=bytes_(E, I // 128, 1, H // 128), ct=bytes_(m.tgmm_xt_cols(T, E) // 128, H, 128),
                                             cs=bytes_(m.tgmm_xt_cols(T, E) // 128, H))),
     "products": (products, lambda: dict(y=nan(T, I), dw=nan(E, H, I))),
     "balance": (balance, lambda: dict(loss=nan(2), counts=ints(2, E), tokens=ints(2), dz=nan(T, E))),
@@ -156,8 +156,9 @@ def test_weights_and_gradients_past_32_bits():
     del q, out, x
     # the weight gradient: ones in the last rows and columns
     cols = m.tgmm_xt_cols(R, E2)
-    a, b = torch.zeros(K, cols, dtype=torch.uint8, device="cuda"), torch.zeros(N, cols, dtype=torch.uint8, device="cuda")
-    a[-3:, 128:128 + R - 1], b[-5:, 128:128 + R - 1] = 0x38, 0x38
+    a, b = (torch.zeros(cols // 128, C, 128, dtype=torch.uint8, device="cuda") for C in (K, N))
+    for t, n in ((a, 3), (b, 5)):                        # 129 rows of the second expert: blocks 1 and 2
+        t[1, -n:], t[2, -n:, :1] = 0x38, 0x38
     dw, ws = torch.full((E2, K, N), 7.0, device="cuda"), m.workspace(m.MOE_OP_TGMM_B128, R, K, N, E2)
     m.moe_tgmm_b128(a, torch.full((cols // 128, K), 127, dtype=torch.uint8, device="cuda"), b,
                     torch.full((cols // 128, N), 127, dtype=torch.uint8, device="cuda"), gs, E2, 0, E2, R, K, N, m.MOE_F32, dw, ws)
@@ -173,8 +174,32 @@ def test_columns_of_tokens_past_32_bits():
     perm = torch.randperm(n * k2, generator=gen(), device="cuda").to(torch.int32)
     gs, M = [500, 0, 700], n * k2
     cols = m.tgmm_xt_cols(M, 3)
-    qt, st, ws = bytes_(C, cols), bytes_(cols // 128, C), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    qt, st, ws = bytes_(cols // 128, C, 128), bytes_(cols // 128, C), torch.zeros(256, dtype=torch.uint8, device="cuda")
     m.moe_quantize_cols_b128(x, None, ld, m.MOE_ACT_NONE, n, k2, perm, dev_i32(gs), 3, 0, 3, M, C, qt, st, ws)
     v = b128.values(host(x.contiguous())[host(perm) // k2])
     oq, os_, used = b128.quantize_cols_b128(v, np.array(gs), 0, 3, M, cols)
-    assert np.array_equal(host(qt)[:, used], oq[:, used]) and np.array_equal(host(st)[used[::128]], os_[used[::128]])
+    assert np.array_equal(b128.columns_of(host(qt))[:, used], oq[:, used]) and np.array_equal(host(st)[used[::128]], os_[used[::128]])
+
+
+def test_blocks_of_rows_past_32_bits():
+    """1100 blocks of 128 rows of 32768 columns: codes past 2^32 bytes, in the quantizer and in the weight gradient."""
+    n, C, N = 1100, 32768, 16
+    M = 128 * n
+    x = torch.zeros(M, C, dtype=torch.bfloat16, device="cuda")
+    x[-128:] = bf(128, C)
+    cols, gs = m.tgmm_xt_cols(M, 1), dev_i32([M])
+    qt, st = torch.empty(cols // 128, C, 128, dtype=torch.uint8, device="cuda"), bytes_(cols // 128, C)
+    ws = m.workspace(m.MOE_OP_TGMM_B128, M, C, N, 1)
+    m.moe_quantize_cols_b128(x, None, C, m.MOE_ACT_NONE, M, 1, None, gs, 1, 0, 1, M, C, qt, st, ws)
+    oq, os_, _ = b128.quantize_cols_b128(b128.values(host(x[-128:])), np.array([128]), 0, 1, 128, 128)
+    assert np.array_equal(b128.columns_of(host(qt[n - 1:n])), oq) and np.array_equal(host(st[n - 1:n]), os_)
+    assert not qt[:n - 1].any() and (st[:n - 1] == 127).all()
+    y, ys = torch.zeros(cols // 128, N, 128, dtype=torch.uint8, device="cuda"), torch.full((cols // 128, N), 127, dtype=torch.uint8, device="cuda")
+    y[n - 1, 3] = 0x38                                   # ones
+    dw = nan(1, C, N)
+    m.moe_tgmm_b128(qt, st, y, ys, gs, 1, 0, 1, M, C, N, m.MOE_F32, dw, ws)
+    want = (e4m3_decode(oq) * b128.scale_values(os_).T).sum(axis=1)
+    # 128 products with codes below 2^9 (exponent 8), each cut below 2^-12 of 2^8, and a float32 sum of 128 terms in chunks of 8
+    lim = b128.scale_values(os_)[0] * (128 * 2.0 ** (8 - 12) + 32 * 2.0 ** -24 * 128 * 512)
+    got = host(dw)[0]
+    assert (np.abs(got[:, 3] - want) <= lim).all() and not np.delete(got, 3, axis=1).any() and m.moe_debug_check(ws) == 0

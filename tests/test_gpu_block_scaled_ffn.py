@@ -144,7 +144,7 @@ def test_stages(case):
 
     def check_cols(t, v):
         q, s, used = b128.quantize_cols_b128(v, gs, g0, El, M, cols)
-        got = host(t.q), host(t.scale)
+        got = b128.columns_of(host(t.q)), host(t.scale)
         assert np.array_equal(got[0][:, used], q[:, used]) and np.array_equal(got[1][used[::128]], s[used[::128]])
         return got
     ht, dyt = check_cols(L.ht, b128.values(ab[:, :I], ab[:, I:])), check_cols(L.dyt, b128.values(dy))
