@@ -37,10 +37,9 @@ struct B128Args {
   int32_t* err;
 };
 
-// The scale operands' bytes: the lowest of ws, byte XB of xs.
-template <int XB = 0>
+// (Of the scale operands the lowest bytes.)
 __device__ __forceinline__ v4f mfma_scaled(const v8i& w, uint32_t ws, const v8i& x, uint32_t xs, const v4f& c) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 0, 0, 0, ws, XB, xs);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 0, 0, 0, ws, 0, xs);
 }
 
 __device__ __forceinline__ v8i frag(const uint4& a, const uint4& b) {
@@ -218,13 +217,6 @@ __device__ __forceinline__ constexpr int frag_col(int f, int n) {
   return OUT_BF16 ? 32 * (f >> 1) + 8 * (n >> 2) + 4 * (f & 1) + (n & 3) : 16 * f + n;
 }
 
-// Row of the tile at staged place r.  gmm: r.  tgmm: of a wave's 128 places, 16 i + n holds row 8 n + i, so that the scales
-// of the eight rows that lane n multiplies are neighbours.
-template <Kind KIND>
-__device__ __forceinline__ int row_at(int r) {
-  return KIND == kTgmm ? (r & ~127) + 8 * (r & 15) + ((r >> 4) & 7) : r;
-}
-
 struct WideTile {
   int row0, col0;                                  // (tgmm: in the group's result)
   int g, rows, steps, blk0;
@@ -282,14 +274,13 @@ struct Cursor {
     }
     const uint32_t stage_at = KIND == kTgmm ? 0u : 128u * s;
     const uint32_t c = 16 * ((lane & 7) ^ (ROWS || !OUT_BF16 ? swz_run(r) : swz_quads(r)));
-    // (64 places further on: tgmm 4 rows, and then the wave's other 128)
-    uint32_t off = (ROWS ? row_at<KIND>(r) : r) * ld + c;
+    uint32_t off = r * ld + c;
     if (KIND != kTgmm && 128 * s + 128 > p.K) off = c < static_cast<uint32_t>(p.K) - 128u * s ? off : 0x80000000u;
     uint8_t* dst = (ROWS ? sm.x[b] : sm.w[b]) + 8 * wave * 128;
 #pragma unroll
     for (int j = 0; j < (ROWS ? kWideRows<KIND> : kWideCols) / 64; ++j)
       if (!ROWS || KIND == kTgmm || 64 * j + 8 * wave < t.rows)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void*)(dst + 64 * 128 * j), 16, off, stage_at + (ROWS ? row_at<KIND>(64 * j) : 64 * j) * ld, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_void*)(dst + 64 * 128 * j), 16, off, stage_at + 64 * j * ld, 0, 0);
     b ^= 1;
     if (++s == t.steps) {
       ++i;
@@ -340,30 +331,42 @@ __device__ __forceinline__ void wide_store(const B128Args& p, const WideTile& t,
   const int64_t left = p.N - c;                    // its columns
   const __amdgpu_buffer_rsrc_t o = buffer(static_cast<uint8_t*>(p.out) + (row0 * p.N + c) * B,
                                           rows > 0 && left > 0 ? (rows - 1) * ld + static_cast<uint32_t>(min(left, static_cast<int64_t>(64))) * B : 0u);
+  const bool odd = l15 & 1;
+  // A lane's two pieces of 16 bytes lie in the two halves of a line of its row.  Neighbouring lanes exchange one, so that a
+  // store writes eight whole lines, of the even lanes' rows and then of the odd ones' (halves of sixteen: weight gradient
+  // 470 us instead of 427, as the L2 takes them).
+  auto put = [&](const v4u32& c0, const v4u32& c1, uint32_t row, int col) {
+    v4u32 a, b;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t other = __builtin_amdgcn_update_dpp(0, odd ? c0[q] : c1[q], 0xb1, 0xf, 0xf, true);    // quad_perm [1, 0, 3, 2]
+      a[q] = odd ? other : c0[q];
+      b[q] = odd ? c1[q] : other;
+    }
+    const bool in = col < left;
+    __builtin_amdgcn_raw_buffer_store_b128(a, o, in ? row + B * col : 0xf0000000u, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(b, o, in ? row + ld + B * col : 0xf0000000u, 0, 0);
+  };
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const uint32_t row = row_at<KIND>(16 * i + l15) * ld;
+    const uint32_t row = (16 * i + (l15 & 14)) * ld;
     v4f v[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f) v[f] = KIND == kGmmF32 ? acc[i][f] * scale : acc[i][f];
     if (OUT_BF16) {
+      v4u32 u[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        v4u32 u;
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const v4f& a = v[2 * h + (q >> 1)];
-          u[q] = pack_bf16(a[2 * (q & 1)], a[2 * (q & 1) + 1]);
+          u[h][q] = pack_bf16(a[2 * (q & 1)], a[2 * (q & 1) + 1]);
         }
-        const int col = 32 * h + 8 * grp;
-        __builtin_amdgcn_raw_buffer_store_b128(u, o, col < left ? row + 2 * col : 0xf0000000u, 0, 0);
-      }
+      put(u[0], u[1], row, (odd ? 32 : 0) + 8 * grp);
     } else {
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        const int col = 16 * f + 4 * grp;
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, v[f]), o, col < left ? row + 4 * col : 0xf0000000u, 0, 0);
-      }
+      for (int h = 0; h < 2; ++h)
+        put(__builtin_bit_cast(v4u32, v[2 * h]), __builtin_bit_cast(v4u32, v[2 * h + 1]), row, 32 * h + (odd ? 16 : 0) + 4 * grp);
     }
   }
 }
@@ -408,7 +411,7 @@ __device__ __forceinline__ void run_wide(const B128Args& p, WideLds<KIND>& sm, S
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int f = 0; f < 4; ++f) acc[i][f] = v4f{0.f, 0.f, 0.f, 0.f};
-  uint32_t xsd[KIND == kTgmm ? 2 : MI];            // scales; gmm: a dword of each row's, four blocks; tgmm: a byte a row
+  uint32_t xsd[MI];                                // scales of the rows; gmm: four blocks of each, tgmm: one
   float unit = 1.0f;                               // float32 scales: what the sums are in units of
 #pragma clang loop unroll(disable)
   for (int s = 0; s < t.steps; ++s) {
@@ -441,10 +444,8 @@ __device__ __forceinline__ void run_wide(const B128Args& p, WideLds<KIND>& sm, S
     v8i x[2];
     x[0] = read_x(0);
     if constexpr (KIND == kTgmm) {
-      static_assert(MI == 8, "rows of 128");
-      const v2i d = lds_read<v2i>(xsb + 256 * sb + 128 * wr + 8 * l15);
-      xsd[0] = d[0];
-      xsd[1] = d[1];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) xsd[i] = lds_read<uint8_t>(xsb + 256 * sb + xr + 16 * i);
     } else if ((sb & 3) == 0) {
 #pragma unroll
       for (int i = 0; i < MI; ++i) xsd[i] = lds_read<uint32_t>(xsb + (xr + 16 * i) * kWindow + sb);
@@ -481,9 +482,9 @@ __device__ __forceinline__ void run_wide(const B128Args& p, WideLds<KIND>& sm, S
 #pragma unroll
         for (int f = 0; f < 4; ++f) acc[i][f] *= ratio;
       }
-      const uint32_t xs = KIND == kTgmm ? xsd[(i >> 2) & 1] : xsd[KIND == kTgmm ? 0 : i] >> shift;
+      const uint32_t xs = xsd[i] >> shift;
 #pragma unroll
-      for (int f = 0; f < 4; ++f) acc[i][f] = mfma_scaled<KIND == kTgmm ? i & 3 : 0>(w[f], wsc[f], x[i & 1], xs, acc[i][f]);
+      for (int f = 0; f < 4; ++f) acc[i][f] = mfma_scaled(w[f], wsc[f], x[i & 1], xs, acc[i][f]);
       __builtin_amdgcn_sched_barrier(0);
     };
     step_barrier();                                // every wave's weights are read
