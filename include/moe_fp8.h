@@ -767,10 +767,11 @@ int moe_quantize_weights_b128(const void* w, int64_t E, int64_t K, int64_t N, ui
  * What lies past the last group's padded end, in both, is not written.
  *   V        the local sorted rows: with perm NULL, x itself, [M, C]; with
  *            perm [T*k] (moe_sort_by_expert's), V[r] = x[perm[start + r] / k],
- *            x [T, C] the tokens, start = sum of group_sizes[0 .. group_offset-1].
+ *            x [T, C] the tokens, start = sum of group_sizes[0 .. first_group-1].
  *   x, x_up, ldx, act as in moe_quantize_rows_b128.  T, k: as in the sort
  *            (k is 1 to 64); without perm T is x's row count, at least M.
- *   group_sizes, E, group_offset, num_local_experts: as in the sort.
+ *   group_sizes, E, first_group, num_local_experts: as in the sort, whose
+ *            group_offset is first_group here and in the products.
  *   M        local rows (rows of the weight gradient's operands).
  *   qt       [cols / 128, C, 128] bytes, scale_t [cols / 128, C] bytes, cols =
  *            moe_tgmm_xt_cols(M, E); both 16-byte aligned.
@@ -780,7 +781,7 @@ int moe_quantize_weights_b128(const void* w, int64_t E, int64_t K, int64_t N, ui
  * MOE_ERR_NULL, MOE_ERR_WORKSPACE.
  */
 int moe_quantize_cols_b128(const void* x, const void* x_up, int64_t ldx, int act, int64_t T, int32_t k, const int32_t* perm,
-                           const int32_t* group_sizes, int32_t E, int32_t group_offset, int32_t num_local_experts,
+                           const int32_t* group_sizes, int32_t E, int32_t first_group, int32_t num_local_experts,
                            int64_t M, int64_t C, uint8_t* qt, uint8_t* scale_t, void* ws, size_t ws_bytes, void* stream);
 
 /*
@@ -804,7 +805,7 @@ int moe_quantize_cols_b128(const void* x, const void* x_up, int64_t ldx, int act
  * lhs_scale, rhs, out 16-byte aligned.  Errors as in moe_gmm_fp8.
  */
 int moe_gmm_b128(const uint8_t* lhs, int64_t ldl, const uint8_t* lhs_scale, int64_t lds, const uint8_t* rhs,
-                 const void* rhs_scale, int rhs_scale_dtype, const int32_t* group_sizes, int32_t E, int32_t group_offset,
+                 const void* rhs_scale, int rhs_scale_dtype, const int32_t* group_sizes, int32_t E, int32_t first_group,
                  int32_t num_local_experts, int64_t M, int64_t K, int64_t N, int out_dtype, void* out, void* ws,
                  size_t ws_bytes, void* stream);
 
@@ -823,7 +824,7 @@ int moe_gmm_b128(const uint8_t* lhs, int64_t ldl, const uint8_t* lhs_scale, int6
  * in moe_tgmm_fp8.
  */
 int moe_tgmm_b128(const uint8_t* lhs_t, const uint8_t* lhs_scale, const uint8_t* rhs_t, const uint8_t* rhs_scale,
-                  const int32_t* group_sizes, int32_t E, int32_t group_offset, int32_t num_local_experts, int64_t M,
+                  const int32_t* group_sizes, int32_t E, int32_t first_group, int32_t num_local_experts, int64_t M,
                   int64_t K, int64_t N, int out_dtype, void* out, void* ws, size_t ws_bytes, void* stream);
 
 /*

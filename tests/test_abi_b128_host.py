@@ -108,3 +108,26 @@ def test_workspaces(lib):
     for bad in ((-1, 1, 8), (2 ** 31, 1, 8), (8, 0, 8), (8, 1, 0), (8, 1, 1025)):
         with pytest.raises(m.MoeError):
             m.workspace_bytes(m.MOE_OP_BALANCE, bad[0], bad[1], 0, bad[2])
+
+
+P, WS = AL, 1 << 30
+WINDOWS = {      # every call here that takes a window of groups, with no rows
+    "moe_quantize_cols_b128": lambda f, w: f(P, None, 64, 0, 0, 2, P, P, *w, 0, 64, P, P, P, WS, None),
+    "moe_gmm_b128": lambda f, w: f(P, 64, P, 16, P, P, m.MOE_E8M0, P, *w, 0, 64, 32, 0, P, P, WS, None),
+    "moe_tgmm_b128": lambda f, w: f(P, P, P, P, P, *w, 0, 64, 32, 0, P, P, WS, None),
+}
+
+
+@pytest.mark.parametrize("name", WINDOWS)
+def test_windows(lib, name):
+    f = getattr(lib, name)
+    big = 2 ** 31 - 1
+    for w in ((8, 4, 5), (8, -1, 2), (8, 2, -1), (8, 9, 0), (8, big, 1), (8, big - 7, 8), (8, 8, big), (1024, big - 1023, 1024), (1, big, big),
+              (0, 0, 0), (1025, 0, 1)):
+        assert WINDOWS[name](f, w) == m.MOE_ERR_SHAPE, w
+
+
+def test_every_call_of_blocks_with_a_window_is_listed():
+    with open(m.HEADER_PATH) as f:
+        decls = [d.split("*/")[-1] for d in f.read().split(";")]
+    assert {d.split("(")[0].split()[-1] for d in decls if "int32_t first_group" in d} == set(WINDOWS)
