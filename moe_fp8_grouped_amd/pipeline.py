@@ -788,12 +788,15 @@ class BlockScaledFFN:
       backward(dout) the gradients ``dx`` [T, H] bf16, ``dw01`` [E_loc, H, 2I]
                      and ``dwo`` [E_loc, I, H] (grad_dtype), and ``dlogits``
                      [T, E]: through the routing weights, plus balance_weight
-                     times the mean of the sequences' losses
+                     times the mean of the sequences' losses (all written, not
+                     added to what the buffers held)
 
     ``w0``, ``w1`` [E_loc, H, I] and ``wo`` [E_loc, I, H] bf16 are quantized
     here and by requantize(); ``x`` [T, H] bf16 and ``logits`` [T, E] (bf16 or
     f32) are the buffers a step reads.  seq_offsets [S + 1] int32: where the
-    packed sequences begin (None: one of T tokens)."""
+    packed sequences begin (None: one of T tokens).  m_cap: room for that many
+    local rows (default T * k); rows past it are dropped, and the workspaces'
+    error words say so."""
 
     def __init__(self, x, logits, w0, w1, wo, k, score=MOE_SCORE_SOFTMAX, renormalize=True, weight_scale=1.0,
                  select_bias=None, group_offset=0, m_cap=None, balance_weight=0.0, seq_offsets=None, grad_dtype=torch.float32):
@@ -835,11 +838,16 @@ class BlockScaledFFN:
         M = T * k
         self.m_cap = Mc = M if m_cap is None else m_cap
         new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
-        self.ids, self.topk_w, self.out = new((T, k), i32), new((T, k), f32), new((T, H), bf)
-        self.perm, self.inv_pos, self.group_sizes = new(M, i32), new(M, i32), new(E, i32)
+        self.out = new((T, H), bf)
+        # until the first step every slot has expert 0, weight 0 and no row: a backward pass then gives zeros
+        fill = lambda n, value, dtype=i32: torch.full(n, value, dtype=dtype, device=dev)
+        self.ids, self.topk_w, self.inv_pos = fill((T, k), 0), fill((T, k), 0.0, f32), fill((M,), -1)
+        self.perm, self.group_sizes = fill((M,), 0), fill((E,), 0)
         self.xq, self.xs, self.hq = B128Rows(T, H, dev), B128Rows(Mc, H, dev), B128Rows(Mc, I, dev)
         self.one = torch.ones((1,), dtype=f32, device=dev)
-        self.ab, self.y = new((Mc, 2 * I), bf), new((Mc, H), bf)
+        self.ab = torch.zeros((Mc, 2 * I), dtype=bf, device=dev)
+        # what the combines gather from has a row for every slot: those past m_cap stay zero
+        self.y, self.dxs = (torch.zeros((max(M, Mc), H), dtype=bf, device=dev) for _ in range(2))
         self.loss, self.counts, self.tokens = (torch.zeros(n, dtype=d, device=dev) for n, d in ((S, f32), ((S, E), i32), (S, i32)))
         self.dloss = torch.full((S,), self.balance_weight / S, dtype=f32, device=dev)
         self.ws_sort = workspace(MOE_OP_SORT_BY_EXPERT, M, 0, 0, E, device=dev)
@@ -847,7 +855,7 @@ class BlockScaledFFN:
         self.ws_down = workspace(MOE_OP_GMM_B128, Mc, I, H, E, device=dev)
         self.ws_balance = workspace(MOE_OP_BALANCE, T, S, 0, E, device=dev)
         # the backward pass
-        self.dy, self.dh, self.dab, self.dxs = (new((Mc, C), bf) for C in (H, I, 2 * I, H))
+        self.dy, self.dh, self.dab = (new((Mc, C), bf) for C in (H, I, 2 * I))
         self.dw = new((T, k), f32)
         self.dyq, self.dabq = B128Rows(Mc, H, dev), B128Rows(Mc, 2 * I, dev)
         self.xt, self.ht, self.dyt, self.dabt = (B128Cols(Mc, C, E, dev) for C in (H, I, H, 2 * I))

@@ -269,3 +269,20 @@ def test_no_tokens_and_no_local_rows():
     for t in (L.out, L.dx, L.dw01, L.dwo, L.dw):
         assert not t.any()
     assert m.moe_debug_check(L.ws_sort) == 0
+
+
+def test_a_backward_pass_before_any_step_and_rows_that_do_not_fit():
+    T, k, E, H, I = 33, 2, 4, 64, 32
+    z, x, w, d = problem(5, T, E, E, H, I)
+    L = layer(z, x, w, k)
+    L.backward(dev_bf16(d))
+    for t in (L.dx, L.dw01, L.dwo, L.dw):
+        assert not t.any()
+    assert m.moe_debug_check(L.ws_dwo) == 0
+    L = layer(z, x, w, k, m_cap=T)                                     # half of the rows: named, and nothing past the buffers
+    L.step()
+    L.backward(dev_bf16(d))
+    torch.cuda.synchronize()
+    assert m.moe_debug_check(L.ws_sort) & m.MOE_DEVERR_ROWS and m.moe_debug_check(L.ws_up) & m.MOE_DEVERR_ROWS
+    for t in (L.out, L.dx, L.dw01, L.dwo):
+        assert torch.isfinite(t.float()).all()
