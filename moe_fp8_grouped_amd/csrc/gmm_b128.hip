@@ -11,6 +11,17 @@
 // operands take the same and the scale is one for all).  The product is formed
 // transposed per 16 x 16 block (the weights are the first operand), so output
 // lane l holds row l%16 and four consecutive columns 4*(l/16) .. +3.
+//
+// Three kernels, by a rule on sizes alone (launch_b128):
+//   few      few pieces of 16 rows (or up to 64) by 16 columns: every weight is met by a row or a few; latency and the
+//            weights' bytes decide.  One row of 7168 x 4096: 8.2 us (29 MB, 3.6 TB/s).
+//   wide     at least a tile for every workgroup: LDS reads (1536 clocks a 256 x 256 x 128 step), its fill (512) and the
+//            matrix instructions (2048) share the time, and few rows leave the weights' bytes.  32768 rows in 64 groups of
+//            2048 x 1536: 140 us (1.5 PFLOP/s); 8192 rows in 32 of 7168 x 4096: 271 us (1.8 PFLOP/s); 128 rows in 64 of
+//            2048 x 1536: 41 us (4.9 TB/s of weights; narrow tiles 44).  tgmm, 32768 rows in 64 groups, 4096 x 1536 bf16
+//            results: 310 us, of which 190 are left without the stores (0.8 GB, 118 us to a plain fill): they do not overlap.
+//   narrow   fewer tiles than that: the latency of a tile's stages.  512 ragged rows in 8 groups of 2080 x 1040: 13 us (wide
+//            tiles 22); 256 rows in 32 groups of 4096 x 1536: 46 us (4.4 TB/s).
 #include <type_traits>
 
 #include "b128_common.hpp"
@@ -191,6 +202,7 @@ __global__ __launch_bounds__(64 * kSplit) void b128_few_kernel(const B128Args p,
 // stage have been on their way since its start.  The stream runs on from tile to
 // tile, under the stores of the last one's results.
 constexpr int kWideThreads = 512, kWideCols = 256, kWindow = 16, kDesc = 64;
+// (gmm: uneven groups of 256 rows on average mostly fit one tile of 320; 288 rows took the slice 294 us where 320 took 291.)
 template <Kind KIND>
 constexpr int kWideRows = KIND == kTgmm ? 256 : 320;
 
