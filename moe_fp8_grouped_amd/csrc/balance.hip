@@ -403,7 +403,9 @@ size_t balance_ws_bytes(int64_t T, int64_t S, int E) {
 
 }  // namespace moe
 
-// sixteen lanes a row up to 128 experts, the whole wave above
+// Sixteen lanes a row up to 128 experts, the whole wave above.  Loss and gradient of 8192 tokens as graphs, us: 64 experts
+// 11.9 and 4.5 (a wave a row 14.2 and 5.7), 128 experts 13.1 and 5.3 (14.6 and 6.0), 256 experts 14.4 and 6.5 (sixteen lanes
+// 14.9 and 7.4); of 32768 tokens, 64 experts, 13.2 and 7.2 (16.1 and 14.1).
 #define MOE_BY_V(CALL, B, S)                                      \
   do {                                                            \
     if (E <= 64) CALL(B, S, 16, 1);                               \
