@@ -12,7 +12,7 @@
 // transposed per 16 x 16 block (the weights are the first operand), so output
 // lane l holds row l%16 and four consecutive columns 4*(l/16) .. +3.
 //
-// Three kernels, by a rule on sizes alone (launch_b128):
+// Three kernels, by a rule on sizes alone (b128_rule.hpp):
 //   few      few pieces of 16 rows (or up to 64) by 16 columns: every weight is met by a row or a few; latency and the
 //            weights' bytes decide.  One row of 7168 x 4096: 8.2 us (29 MB, 3.6 TB/s).
 //   wide     at least a tile for every workgroup: LDS reads (1536 clocks a 256 x 256 x 128 step), its fill (512) and the
@@ -25,6 +25,7 @@
 #include <type_traits>
 
 #include "b128_common.hpp"
+#include "b128_rule.hpp"
 #include "stage_common.hpp"
 
 namespace moe {
@@ -201,10 +202,11 @@ __global__ __launch_bounds__(64 * kSplit) void b128_few_kernel(const B128Args p,
 // follows, the weights two stages on take their place, while the rows of the next
 // stage have been on their way since its start.  The stream runs on from tile to
 // tile, under the stores of the last one's results.
-constexpr int kWideThreads = 512, kWideCols = 256, kWindow = 16, kDesc = 64;
-// (gmm: uneven groups of 256 rows on average mostly fit one tile of 320; 288 rows took the slice 294 us where 320 took 291.)
+constexpr int kWideThreads = 512, kWindow = 16, kDesc = 64;
+using b128::kNarrow;
+using b128::kWideCols;
 template <Kind KIND>
-constexpr int kWideRows = KIND == kTgmm ? 256 : 320;
+constexpr int kWideRows = KIND == kTgmm ? b128::kWideRowsTgmm : b128::kWideRowsGmm;
 
 template <Kind KIND>
 struct WideLds {
@@ -620,7 +622,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_wide_kernel(const B128Ar
 // columns; eight stages of both operands in LDS, seven ahead, the stream running on from
 // tile to tile: for fewer rows or tiles than the wide ones fill the GPU with, where
 // the loads' latency is the time.  Each stage brings its scales.
-constexpr int kNarrow = 64, kNarrowStages = 8, kNarrowDesc = 256;
+constexpr int kNarrowStages = 8, kNarrowDesc = 256;
 
 struct NarrowLds {
   uint8_t x[kNarrowStages][kNarrow * 128];
@@ -846,38 +848,24 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_narrow_kernel(const B128
   if constexpr (!TG) zero_rows<OUT_BF16, kWideThreads>(p, n_rows);
 }
 
-// Workgroups of the few-rows kernel with 16 MI rows a tile.
-template <int MI>
-int64_t few_tiles(const B128Args& p) {
-  const int64_t groups = p.El < p.M ? p.El : p.M;
-  return p.El == 1 ? moe_cdiv(p.M, 16 * MI) : p.M / (16 * MI) + groups + 1;
-}
 template <Kind KIND, bool OUT_BF16, int MI>
-bool few(const B128Args& p, hipStream_t st) {
-  const int64_t tiles = few_tiles<MI>(p), grid = tiles * (p.N / 16);
-  // As long as its 16 x 16 pieces are at most six a CU.  One group of 7168 by 4096: 1 row 8.2 us (narrow tiles 27), 64 rows
-  // 23 (33), 128 rows 42 (33); 64 groups of 2048 by 1536: 8 rows 11 (12), 16 rows 19 (19), 32 rows 31 (26).
-  if (grid * MI > 6 * num_cus()) return false;
-  b128_few_kernel<KIND, OUT_BF16, MI><<<static_cast<unsigned>(grid), 64 * kSplit, 0, st>>>(p, static_cast<int>(tiles));
-  return true;
+void launch_few(const B128Args& p, hipStream_t st) {
+  const int64_t tiles = b128::few_tiles(p.El, p.M, 16 * MI);
+  b128_few_kernel<KIND, OUT_BF16, MI><<<static_cast<unsigned>(tiles * (p.N / 16)), 64 * kSplit, 0, st>>>(p, static_cast<int>(tiles));
 }
 
 template <Kind KIND, bool OUT_BF16>
 hipError_t launch_b128(const B128Args& p, hipStream_t st) {
-  const int64_t groups = p.El < p.M ? p.El : p.M, cols = moe_cdiv(p.N, kWideCols);
-  const int64_t tiles = KIND == kTgmm ? p.El * moe_cdiv(p.K, kWideRows<KIND>) * cols : (groups + p.M / kWideRows<KIND>) * cols;
-  if constexpr (KIND != kTgmm) {
-    const bool one = p.El == 1;
-    if (one && p.M > 32 ? few<KIND, OUT_BF16, 4>(p, st) : one && p.M > 16 ? few<KIND, OUT_BF16, 2>(p, st) : few<KIND, OUT_BF16, 1>(p, st))
-      return hipGetLastError();
-  }
-  // Wide tiles where every workgroup has one: 128 rows in 64 groups of 2048 x 1536 take 41 us (narrow ones 44 to 47), the weight
-  // gradient of 512 rows in 8 groups, 2080 x 1040, 19 us (narrow ones 29); 512 rows in 8 groups of 2080 x 1040, 20 tiles, take 13 us
-  // with narrow ones (19).
-  if (tiles >= num_cus())
+  const b128::Choice c = KIND == kTgmm ? b128::gradient_kernel(p.El, p.K, p.N, num_cus()) : b128::product_kernel(p.El, p.M, p.N, num_cus());
+  if (c == b128::kWideTiles) {
     b128_wide_kernel<KIND, OUT_BF16><<<num_cus(), kWideThreads, 0, st>>>(p);
-  else
+  } else if (c == b128::kNarrowTiles) {
     b128_narrow_kernel<KIND, OUT_BF16><<<num_cus(), kWideThreads, 0, st>>>(p);
+  } else if constexpr (KIND != kTgmm) {
+    if (c == b128::kFew64) launch_few<KIND, OUT_BF16, 4>(p, st);
+    else if (c == b128::kFew32) launch_few<KIND, OUT_BF16, 2>(p, st);
+    else launch_few<KIND, OUT_BF16, 1>(p, st);
+  }
   return hipGetLastError();
 }
 
