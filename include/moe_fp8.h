@@ -796,7 +796,9 @@ int moe_quantize_cols_b128(const void* x, const void* x_up, int64_t ldx, int act
  *   rhs      [E_loc, N, K] e4m3fn; rhs_scale [E_loc, ceil(K/128), 1,
  *            ceil(N/128)], of rhs_scale_dtype MOE_E8M0
  *            (moe_quantize_weights_b128) or MOE_F32 (any float32: weights as
- *            moe_quantize_weights or a checkpoint hold them in 128 x 128 blocks).
+ *            moe_quantize_weights or a checkpoint hold them in 128 x 128 blocks;
+ *            a scale that is not finite is NaN, as 255 is; a block of scale 0
+ *            adds nothing, but NaN where it holds or meets one).
  *   group_sizes .. num_local_experts, out, out_dtype as in moe_gmm_fp8.  One
  *            group (E = 1, its size M) is a plain linear layer.
  *   ws       workspace of moe_workspace_bytes(MOE_OP_GMM_B128, M, K, N, E).

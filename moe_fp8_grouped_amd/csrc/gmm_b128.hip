@@ -59,6 +59,27 @@ __device__ __forceinline__ v8i frag(const uint4& a, const uint4& b) {
              static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w)};
 }
 
+// A float32 scale as a power of two, which the matrix core applies to the products' exponents, times a factor in [1, 2) with
+// the scale's sign: no block's sum leaves float32's range where scale times sum stays in it.  What a subnormal lies below
+// e8m0's smallest power comes off the rows' codes (by `down`; a code that would fall below 0 belongs to results that are 0
+// in float32 either way), and a scale of 0 takes them all to the lowest: such a block adds nothing, or NaN for a NaN in it.
+// A scale that is not finite is NaN.
+struct F32Scale {
+  uint32_t code, down;
+  float factor;
+};
+__device__ __forceinline__ F32Scale split_scale(uint32_t v) {
+  const uint32_t e = (v >> 23) & 255u, f = v & 0x7fffffu, lz = __builtin_clz(f | 1u);
+  const uint32_t one = (v & 0x80000000u) | 0x3f800000u;
+  if (e == 255u) return {255u, 0u, 1.0f};
+  if (e != 0u) return {e, 0u, __uint_as_float(one | f)};
+  if (f == 0u) return {0u, 255u, 1.0f};
+  return {0u, lz - 9u, __uint_as_float(one | ((f << (lz - 8u)) & 0x7fffffu))};
+}
+__device__ __forceinline__ uint32_t lowered(uint32_t code, uint32_t down) {
+  return code == 255u ? code : __builtin_elementwise_sub_sat(code, down);
+}
+
 // Two values to bfloat16, nearest even, in one operation (f32_to_bf16 takes eight for each).
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef float v2f __attribute__((ext_vector_type(2)));
@@ -149,7 +170,6 @@ __global__ __launch_bounds__(64 * kSplit) void b128_few_kernel(const B128Args p,
   for (int b0 = wave * per; b0 < end; b0 += AHEAD) {
     uint4 w[AHEAD][2], x[AHEAD][MI][2];
     uint32_t xsc[AHEAD][MI], wsc[AHEAD];
-    float wf[AHEAD];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
       if (b0 + u >= end) continue;
@@ -164,7 +184,7 @@ __global__ __launch_bounds__(64 * kSplit) void b128_few_kernel(const B128Args p,
       for (int i = 0; i < MI; ++i) xsc[u][i] = 16 * i + l15 < there ? xs[16 * i * p.lds + b0 + u] : 0;
       const int64_t at = ws0 + static_cast<int64_t>(b0 + u) * nb;
       if (KIND == kGmmF32)
-        wf[u] = static_cast<const float*>(p.ws)[at];
+        wsc[u] = static_cast<const uint32_t*>(p.ws)[at];
       else
         wsc[u] = static_cast<const uint8_t*>(p.ws)[at];
     }
@@ -174,9 +194,10 @@ __global__ __launch_bounds__(64 * kSplit) void b128_few_kernel(const B128Args p,
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         const v8i wv = frag(w[u][0], w[u][1]), xv = frag(x[u][i][0], x[u][i][1]);
-        if constexpr (KIND == kGmmF32)
-          acc[i] += wf[u] * mfma_scaled(wv, 127, xv, xsc[u][i], v4f{0.f, 0.f, 0.f, 0.f});
-        else
+        if constexpr (KIND == kGmmF32) {
+          const F32Scale sc = split_scale(wsc[u]);
+          acc[i] += sc.factor * mfma_scaled(wv, sc.code, xv, lowered(xsc[u][i], sc.down), v4f{0.f, 0.f, 0.f, 0.f});
+        } else
           acc[i] = mfma_scaled(wv, wsc[u], xv, xsc[u][i], acc[i]);
       }
     }
@@ -470,24 +491,18 @@ __device__ __forceinline__ void run_wide(const B128Args& p, WideLds<KIND>& sm, S
       const uint32_t byte = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.ws)) + (static_cast<uint32_t>(t.g) * t.steps + s) * nb + c) & 3;
       wsc[0] = wsc[1] = wsc[2] = wsc[3] = lds_read<uint8_t>(wsb + 8 * sb + 4 * (wc >> 1) + byte);
     }
-    if constexpr (KIND == kGmmF32) {
-      // The scale is a power of two, which the matrix core applies, times a factor in [1, 2) (or below, for a subnormal):
-      // the sums are held in units of the last block's factor, and change units by the ratio of two.
-      const uint32_t v = __builtin_amdgcn_readfirstlane(lds_read<uint32_t>(wsb + 8 * sb + 4 * (wc >> 1)));
-      const uint32_t e = (v >> 23) & 255u;
-      float m = __uint_as_float((v & 0x807fffffu) | 0x3f800000u);
-      if (e == 0u) m = __uint_as_float(v) * 0x1p127f;
-      if (e == 255u) m = 1.0f;                     // (its results are NaN)
-      if (m == 0.0f) {                             // a block of scale 0: no sum changes
-        m = unit;
-#pragma unroll
-        for (int f = 0; f < 4; ++f) w[f] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
-      }
-      if (s > 0) ratio = unit / m;
-      unit = m;
-      wsc[0] = wsc[1] = wsc[2] = wsc[3] = e;
-    }
     const uint32_t shift = KIND == kTgmm ? 0 : 8 * (sb & 3);
+    if constexpr (KIND == kGmmF32) {
+      // The sums are held in units of the last block's factor, and change units by the ratio of two.
+      const F32Scale sc = split_scale(__builtin_amdgcn_readfirstlane(lds_read<uint32_t>(wsb + 8 * sb + 4 * (wc >> 1))));
+      if (s > 0) ratio = unit / sc.factor;
+      unit = sc.factor;
+      wsc[0] = wsc[1] = wsc[2] = wsc[3] = sc.code;
+      if (sc.down) {                               // (rare: the stage's codes of the rows, in their places)
+#pragma unroll
+        for (int i = 0; i < MI; ++i) xsd[i] = (xsd[i] & ~(255u << shift)) | lowered((xsd[i] >> shift) & 255u, sc.down) << shift;
+      }
+    }
     auto block = [&](auto i_c) {
       constexpr int i = decltype(i_c)::value;
       if (i + 1 < MI) x[(i + 1) & 1] = read_x(i + 1);
@@ -800,7 +815,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_narrow_kernel(const B128
           const v8i x = frag(__builtin_bit_cast(uint4, lds_read<v4i>(xa)), __builtin_bit_cast(uint4, lds_read<v4i>(xa ^ 64u)));
           const uint32_t xsa = lds_addr(sm.xs[0]) + b * static_cast<uint32_t>(sizeof(sm.xs[0])), wsa = lds_addr(sm.ws[0]) + b * static_cast<uint32_t>(sizeof(sm.ws[0]));
           uint32_t xs, ws[2];
-          float wf = 1.0f;
+          float factor = 1.0f;
           if constexpr (TG) {
             xs = lds_read<uint8_t>(xsa + 16 * wr + l15);
 #pragma unroll
@@ -808,8 +823,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_narrow_kernel(const B128
           } else {
             xs = lds_read<uint32_t>(xsa + 4 * (16 * wr + l15)) >> (8 * (s & 3));
             if constexpr (KIND == kGmmF32) {
-              wf = lds_read<float>(wsa);
-              ws[0] = ws[1] = 127;
+              const F32Scale sc = split_scale(lds_read<uint32_t>(wsa));
+              factor = sc.factor;
+              xs = lowered(xs & 255u, sc.down);
+              ws[0] = ws[1] = sc.code;
             } else {
               const uint32_t byte = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.ws)) + (static_cast<uint32_t>(t.g) * t.steps + s) * nb + t.col0 / 128) & 3;
               ws[0] = ws[1] = lds_read<uint8_t>(wsa + byte);
@@ -820,7 +837,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_narrow_kernel(const B128
             const uint32_t at = frag_col<OUT_BF16>(f, 0) * 128;
             const v8i w = frag(__builtin_bit_cast(uint4, lds_read<v4i>(wa + at)), __builtin_bit_cast(uint4, lds_read<v4i>((wa ^ 64u) + at)));
             if constexpr (KIND == kGmmF32)
-              acc[f] += wf * mfma_scaled(w, 127, x, xs, v4f{0.f, 0.f, 0.f, 0.f});
+              acc[f] += factor * mfma_scaled(w, ws[f], x, xs, v4f{0.f, 0.f, 0.f, 0.f});
             else
               acc[f] = mfma_scaled(w, ws[f], x, xs, acc[f]);
           }
