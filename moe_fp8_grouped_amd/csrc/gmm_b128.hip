@@ -35,6 +35,11 @@ using namespace stage;
 
 enum Kind { kGmmE8M0, kGmmF32, kTgmm };
 
+// What the calls accept, and the offsets inside a tile count on: K, N and the rows' stride; the stride of their scales.
+constexpr int64_t kMaxLength = 1 << 22, kMaxScaleStride = 1 << 23;
+// Offsets that lie outside every buffer: of a load, and of a store (whose buffers are larger).
+constexpr uint32_t kNowhere = 0x80000000u, kNoStore = 0xf0000000u;
+
 struct B128Args {
   const uint8_t* x;            // gmm: rows [M, K]; tgmm: [cols / 128, K, 128]
   int64_t ldx;
@@ -175,7 +180,7 @@ __global__ __launch_bounds__(64 * kSplit) void b128_few_kernel(const B128Args p,
       if (b0 + u >= end) continue;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {                // chunks past K, and rows past those there are, lie outside the buffers: zeros
-        const uint32_t at = 128u * (b0 + u) + 64 * h + 16 * grp, o = at < K ? at : 0x80000000u;
+        const uint32_t at = 128u * (b0 + u) + 64 * h + 16 * grp, o = at < K ? at : kNowhere;
         w[u][h] = buffer_load16(wbuf, l15 * K + o, 0);
 #pragma unroll
         for (int i = 0; i < MI; ++i) x[u][i][h] = buffer_load16(xbuf, (16 * i + l15) * ldx + o, 0);
@@ -238,6 +243,8 @@ struct WideLds {
   int4 desc[kDesc];                                // first row, column tile, group, rows
   int2 more[kDesc];                                // blocks, first block
 };
+static_assert(kWideRows<kGmmE8M0> * kMaxLength <= kNowhere && kWideCols * kMaxLength <= kNowhere &&
+              kWideRows<kGmmE8M0> * kMaxScaleStride < (int64_t{1} << 32), "offsets of a tile's operands");
 static_assert(sizeof(WideLds<kGmmE8M0>) <= 160 * 1024 && sizeof(WideLds<kTgmm>) <= 160 * 1024, "LDS of a CU");
 
 // Slot of 16-byte chunk c of a staged row r: c ^ swizzle(r).  Rows of even and odd number lie in different halves of
@@ -310,7 +317,7 @@ struct Cursor {
     const uint32_t stage_at = KIND == kTgmm ? 0u : 128u * s;
     const uint32_t c = 16 * ((lane & 7) ^ (ROWS || !OUT_BF16 ? swz_run(r) : swz_quads(r)));
     uint32_t off = r * ld + c;
-    if (KIND != kTgmm && 128 * s + 128 > p.K) off = c < static_cast<uint32_t>(p.K) - 128u * s ? off : 0x80000000u;
+    if (KIND != kTgmm && 128 * s + 128 > p.K) off = c < static_cast<uint32_t>(p.K) - 128u * s ? off : kNowhere;
     uint8_t* dst = (ROWS ? sm.x[b] : sm.w[b]) + 8 * wave * 128;
 #pragma unroll
     for (int j = 0; j < (ROWS ? kWideRows<KIND> : kWideCols) / 64; ++j)
@@ -362,7 +369,9 @@ __device__ __forceinline__ void wide_store(const B128Args& p, const WideTile& t,
   const int l15 = lane & 15, grp = lane >> 4, wr = wave >> 2, wc = wave & 3;
   const uint32_t ld = static_cast<uint32_t>(p.N) * B;
   const int64_t c = t.col0 + 64 * wc, row0 = (KIND == kTgmm ? t.g * p.K + t.row0 : t.row0) + 16 * MI * wr;
-  const int rows = t.rows - 16 * MI * wr;          // the wave's rows (or none)
+  const int rows = min(t.rows - 16 * MI * wr, 16 * MI);    // the wave's rows (or none)
+  // 32 bits hold every offset, and no buffer reaches the stores that go nowhere (of the whole tile's rows it would)
+  static_assert(16 * MI * kMaxLength * B + 64 * B <= kNoStore, "offsets of a wave's results");
   const int64_t left = p.N - c;                    // its columns
   const __amdgpu_buffer_rsrc_t o = buffer(static_cast<uint8_t*>(p.out) + (row0 * p.N + c) * B,
                                           rows > 0 && left > 0 ? (rows - 1) * ld + static_cast<uint32_t>(min(left, static_cast<int64_t>(64))) * B : 0u);
@@ -379,8 +388,8 @@ __device__ __forceinline__ void wide_store(const B128Args& p, const WideTile& t,
       b[q] = odd ? c1[q] : other;
     }
     const bool in = col < left;
-    __builtin_amdgcn_raw_buffer_store_b128(a, o, in ? row + B * col : 0xf0000000u, 0, 0);
-    __builtin_amdgcn_raw_buffer_store_b128(b, o, in ? row + ld + B * col : 0xf0000000u, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(a, o, in ? row + B * col : kNoStore, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(b, o, in ? row + ld + B * col : kNoStore, 0, 0);
   };
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
@@ -749,8 +758,8 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_narrow_kernel(const B128
       uint32_t xo = lr * ldx + xc, wo = lr * ldw + wch;
       if (!TG && 128 * ls + 128 > p.K) {
         const uint32_t end = static_cast<uint32_t>(p.K) - 128u * ls;
-        xo = xc < end ? xo : 0x80000000u;
-        wo = wch < end ? wo : 0x80000000u;
+        xo = xc < end ? xo : kNowhere;
+        wo = wch < end ? wo : kNowhere;
       }
       const uint32_t at = TG ? 0u : 128u * ls;
       if constexpr (TG) {
@@ -906,10 +915,10 @@ extern "C" int moe_gmm_b128(const uint8_t* lhs, int64_t ldl, const uint8_t* lhs_
     return MOE_ERR_SHAPE;
   // row offsets inside a tile, and a group's weights' scales, are 32-bit; a tile's rows span less than 2^31 bytes, so that
   // chunks past K, at 2^31, lie outside its buffer
-  if (M > INT32_MAX - 1 || K > (1 << 22) || ldl > (1 << 22) || N > (1 << 22) || N * moe_cdiv(K, 128) > INT32_MAX) return MOE_ERR_SHAPE;
+  if (M > INT32_MAX - 1 || K > moe::kMaxLength || ldl > moe::kMaxLength || N > moe::kMaxLength || N * moe_cdiv(K, 128) > INT32_MAX) return MOE_ERR_SHAPE;
   // the tile table of any split of M rows into the groups stays below 2^31 entries
   if ((moe_cdiv(M, 16) + num_local_experts + 1) * (N / 16) > INT32_MAX) return MOE_ERR_SHAPE;
-  if (ldl < K || ldl % 16 || lds < moe_cdiv(K, 128) || lds % 16 || lds > (1 << 23)) return MOE_ERR_SHAPE;
+  if (ldl < K || ldl % 16 || lds < moe_cdiv(K, 128) || lds % 16 || lds > moe::kMaxScaleStride) return MOE_ERR_SHAPE;
   if (rhs_scale_dtype != MOE_E8M0 && rhs_scale_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
   if (out_dtype == MOE_DTYPE_DEFAULT || out_dtype == MOE_E4M3FN) out_dtype = MOE_BF16;
   if (out_dtype != MOE_BF16 && out_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
@@ -936,7 +945,7 @@ extern "C" int moe_tgmm_b128(const uint8_t* lhs_t, const uint8_t* lhs_scale, con
                              const int32_t* group_sizes, int32_t E, int32_t group_offset, int32_t num_local_experts, int64_t M,
                              int64_t K, int64_t N, int out_dtype, void* out, void* ws, size_t ws_bytes, void* stream) {
   using moe::tile::kMaxLocal;
-  if (M < 0 || K <= 0 || N <= 0 || K % 16 || N % 16 || K > (1 << 22) || N > (1 << 22)) return MOE_ERR_SHAPE;
+  if (M < 0 || K <= 0 || N <= 0 || K % 16 || N % 16 || K > moe::kMaxLength || N > moe::kMaxLength) return MOE_ERR_SHAPE;
   if (E <= 0 || E > 1024 || group_offset < 0 || num_local_experts < 0 || num_local_experts > kMaxLocal ||
       group_offset > E - num_local_experts)
     return MOE_ERR_SHAPE;
