@@ -49,9 +49,13 @@ __device__ __forceinline__ uint4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_
   return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, add, 0));
 }
 
-// A group of m rows: as few tiles as hold them, evenly filled with blocks of 16.
-__device__ __forceinline__ int row_tiles(int m, int most) { return (m + most - 1) / most; }
-__device__ __forceinline__ int tile_frags(int m, int nb) { return ((m + 15) / 16 + nb - 1) / nb; }
+// A group of m rows: as few tiles as hold them, evenly filled with blocks of 16.  (m may be all of 2^31 - 1: the sums are unsigned.)
+__device__ __forceinline__ int row_tiles(int m, int most) {
+  return static_cast<int>((static_cast<uint32_t>(m) + static_cast<uint32_t>(most) - 1u) / static_cast<uint32_t>(most));
+}
+__device__ __forceinline__ int tile_frags(int m, int nb) {
+  return static_cast<int>(((static_cast<uint32_t>(m) + 15u) / 16u + static_cast<uint32_t>(nb) - 1u) / static_cast<uint32_t>(nb));
+}
 
 }  // namespace stage
 }  // namespace moe

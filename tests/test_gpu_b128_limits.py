@@ -40,3 +40,25 @@ def test_float32_weight_gradient_of_the_widest_rows():
                 for v in (lambda a: a.view(F8).double(), lambda a: a.view(F8).double().abs(), exponents)]
         check(dw[0, :, c:e], *sums, 128, False, c)
     assert m.moe_debug_check(work) == 0
+
+
+def test_the_most_rows():
+    """2^31 - 2 rows of 16 by 16: their results past 2^36 bytes, the last tile's rows past 2^31 - 320."""
+    M, K, N, g = 2 ** 31 - 2, 16, 16, gen(3)
+    at = torch.tensor([0, 321, 2 ** 30 + 5, M - 337, M - 320, M - 17, M - 1], device="cuda")
+    x = torch.zeros(M, K, dtype=torch.uint8, device="cuda")
+    rows, w, ws = codes(g, len(at), K), codes(g, 1, N, K), e8m0(g, 115, 124, 1, 1, 1)
+    rows[:, 0], w[0, :, 0] = 0x38, 0x38                     # no row of zeros
+    for i, r in enumerate(at.tolist()):
+        x[r] = rows[i]
+    xs = torch.full((M, 16), 125, dtype=torch.uint8, device="cuda")
+    out, work = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda"), m.workspace(m.MOE_OP_GMM_B128, M, K, N, 1)
+    m.moe_gmm_b128(x, K, xs, 16, w, ws, m.MOE_E8M0, dev_i32([M]), 1, 0, 1, M, K, N, m.MOE_BF16, out, work)
+    assert m.moe_debug_check(work) == 0
+    del x, xs
+    found = []
+    for a in range(0, M, 1 << 26):
+        found += [a + i for i in (out[a:a + (1 << 26)] != 0).any(dim=1).nonzero()[:, 0].tolist()[:100]]
+    assert found == at.tolist()
+    got = torch.cat([out[r:r + 1] for r in found])
+    check(got, *block_sums(rows, torch.full((len(at), 1), 125, dtype=torch.uint8, device="cuda"), w[0], ws[0]), K, True, "rows")
