@@ -110,6 +110,52 @@ __device__ __forceinline__ void zero_rows(const B128Args& p, int64_t n_rows) {
     *reinterpret_cast<uint4*>(z + i) = make_uint4(0, 0, 0, 0);
 }
 
+// The local groups' rows and tiles (tgmm: blocks) of tiles with up to ROWS rows, for the kernels that decode tiles: in the
+// stages' LDS, which is free while they do.
+struct Table {
+  int rows_off[kMaxLocal + 1], tiles_off[kMaxLocal + 1], blocks_off[kMaxLocal + 1], tmp[kMaxLocal];
+};
+template <Kind KIND, int ROWS>
+__device__ __forceinline__ void group_table(const B128Args& p, Table& gt, int tid, int threads, int col_tiles) {
+  for (int g = tid; g < p.El; g += threads) {
+    int m = p.sizes[p.g0 + g];
+    if (m < 0) {
+      if (blockIdx.x == 0) raise_error(p.err, MOE_DEVERR_GROUP_SIZE);
+      m = 0;
+    }
+    gt.tmp[g] = m;
+  }
+  __syncthreads();
+  const bool over = wave0_scan_sat(gt.tmp, gt.rows_off, p.El, p.M);
+  if (over && tid == 0 && blockIdx.x == 0) raise_error(p.err, MOE_DEVERR_ROWS);
+  __syncthreads();
+  for (int g = tid; g < p.El; g += threads) {
+    const int m = gt.rows_off[g + 1] - gt.rows_off[g];
+    gt.tmp[g] = KIND == kTgmm ? (m + 127) / 128 : row_tiles(m, ROWS) * col_tiles;
+  }
+  __syncthreads();
+  wave0_scan(gt.tmp, KIND == kTgmm ? gt.blocks_off : gt.tiles_off, p.El);
+  __syncthreads();
+}
+
+// Tile t: first row (tgmm: in the group's result), column tile, group, rows; blocks of the contraction, first block.
+template <Kind KIND, int ROWS>
+__device__ __forceinline__ void decode_tile(const B128Args& p, const Table& gt, int t, int row_tiles_tgmm, int col_tiles, int4& desc, int2& more) {
+  if (KIND == kTgmm) {
+    const int g = t / (row_tiles_tgmm * col_tiles), l = t - g * row_tiles_tgmm * col_tiles, rt = l / col_tiles, ct = l - rt * col_tiles;
+    desc = make_int4(ROWS * rt, ct, g, min(ROWS, static_cast<int>(p.K) - ROWS * rt));
+    more = make_int2(gt.blocks_off[g + 1] - gt.blocks_off[g], gt.blocks_off[g]);
+  } else {
+    const int g = find_group(gt, p.El, t);
+    const int m = gt.rows_off[g + 1] - gt.rows_off[g], nr = row_tiles(m, ROWS), fr = tile_frags(m, nr);
+    const int local = t - gt.tiles_off[g], ct = local / nr, rt = local - ct * nr;
+    // (even filling may leave a last tile without rows: it has no stages)
+    const int rows = max(min(16 * fr, m - 16 * fr * rt), 0);
+    desc = make_int4(gt.rows_off[g] + 16 * fr * rt, ct, g, rows);
+    more = make_int2(rows ? static_cast<int>((p.K + 127) / 128) : 0, 0);
+  }
+}
+
 // ---------------------------------------------------------------- few rows
 // 16 MI rows by 16 columns a workgroup: the weights of sixteen columns are a
 // stream of K bytes each, its blocks dealt out to eight waves, a wave's loads of
@@ -548,10 +594,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_wide_kernel(const B128Ar
   constexpr bool TG = KIND == kTgmm;
   constexpr int ROWS = kWideRows<KIND>;
   const int NT = static_cast<int>((p.N + kWideCols - 1) / kWideCols), RT = TG ? static_cast<int>((p.K + ROWS - 1) / ROWS) : 0;
-  // the group table lives in the stages while tiles are decoded, up to kDesc at a time
-  struct Table {
-    int rows_off[kMaxLocal + 1], tiles_off[kMaxLocal + 1], blocks_off[kMaxLocal + 1], tmp[kMaxLocal];
-  };
+  // tiles are decoded up to kDesc at a time
   static_assert(sizeof(Table) <= sizeof(sm.x), "the group table fits the stages");
   Table& gt = *reinterpret_cast<Table*>(&sm.x[0][0]);
   int first = 0, last = 0, step = 1, n_rows = 0;
@@ -559,45 +602,12 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_wide_kernel(const B128Ar
   for (int base = 0;; base += kDesc) {
     const int tid = opaque(threadIdx.x);
     __syncthreads();
-    for (int g = tid; g < p.El; g += kWideThreads) {
-      int m = p.sizes[p.g0 + g];
-      if (m < 0) {
-        if (blockIdx.x == 0) raise_error(p.err, MOE_DEVERR_GROUP_SIZE);
-        m = 0;
-      }
-      gt.tmp[g] = m;
-    }
-    __syncthreads();
-    const bool over = wave0_scan_sat(gt.tmp, gt.rows_off, p.El, p.M);
-    if (over && tid == 0 && blockIdx.x == 0) raise_error(p.err, MOE_DEVERR_ROWS);
-    __syncthreads();
-    for (int g = tid; g < p.El; g += kWideThreads) {
-      const int m = gt.rows_off[g + 1] - gt.rows_off[g];
-      gt.tmp[g] = TG ? (m + 127) / 128 : row_tiles(m, ROWS) * NT;
-    }
-    __syncthreads();
-    wave0_scan(gt.tmp, TG ? gt.blocks_off : gt.tiles_off, p.El);
-    __syncthreads();
+    group_table<KIND, ROWS>(p, gt, tid, kWideThreads, NT);
     xcd_share(TG ? p.El * RT * NT : gt.tiles_off[p.El], first, last, step);
     n_rows = gt.rows_off[p.El];
     const int left = first < last ? (last - first + step - 1) / step - base : 0;       // this workgroup's tiles
     const int count = min(left, kDesc);
-    if (tid < count) {
-      const int t = first + (base + tid) * step;
-      if (TG) {
-        const int g = t / (RT * NT), l = t - g * RT * NT, rt = l / NT, ct = l - rt * NT;
-        sm.desc[tid] = make_int4(ROWS * rt, ct, g, min(ROWS, static_cast<int>(p.K) - ROWS * rt));
-        sm.more[tid] = make_int2(gt.blocks_off[g + 1] - gt.blocks_off[g], gt.blocks_off[g]);
-      } else {
-        const int g = find_group(gt, p.El, t);
-        const int m = gt.rows_off[g + 1] - gt.rows_off[g], nb = row_tiles(m, ROWS), fr = tile_frags(m, nb);
-        const int local = t - gt.tiles_off[g], ct = local / nb, rt = local - ct * nb;
-        // (even filling may leave a last tile without rows: it has no stages)
-        const int rows = max(min(16 * fr, m - 16 * fr * rt), 0);
-        sm.desc[tid] = make_int4(gt.rows_off[g] + 16 * fr * rt, ct, g, rows);
-        sm.more[tid] = make_int2(rows ? static_cast<int>((p.K + 127) / 128) : 0, 0);
-      }
-    }
+    if (tid < count) decode_tile<KIND, ROWS>(p, gt, first + (base + tid) * step, RT, NT, sm.desc[tid], sm.more[tid]);
     __syncthreads();
     if (count > 0) {
       const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -646,7 +656,9 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_wide_kernel(const B128Ar
 // columns; eight stages of both operands in LDS, seven ahead, the stream running on from
 // tile to tile: for fewer rows or tiles than the wide ones fill the GPU with, where
 // the loads' latency is the time.  Each stage brings its scales.
-constexpr int kNarrowStages = 8, kNarrowDesc = 256;
+// Fewer than one wide tile a workgroup are fewer than 20 narrow ones (gmm: 64 rows for 320, 64 columns for 256, and a group's
+// last tile; tgmm: 16), so at most 24 after the split over the XCDs, 42 on a device of 15 CUs.
+constexpr int kNarrowStages = 8, kNarrowDesc = 64;
 
 struct NarrowLds {
   uint8_t x[kNarrowStages][kNarrow * 128];
@@ -670,206 +682,164 @@ __global__ __launch_bounds__(kWideThreads, 2) void b128_narrow_kernel(const B128
   constexpr bool TG = KIND == kTgmm;
   constexpr int NST = kNarrowStages;
   const int NT = static_cast<int>((p.N + kNarrow - 1) / kNarrow), RT = TG ? static_cast<int>((p.K + kNarrow - 1) / kNarrow) : 0;
-  // the group table lives in the stages while tiles are decoded, up to kNarrowDesc at a time
-  struct Table {
-    int rows_off[kMaxLocal + 1], tiles_off[kMaxLocal + 1], blocks_off[kMaxLocal + 1], tmp[kMaxLocal];
-  };
   static_assert(sizeof(Table) <= sizeof(sm.x), "the group table fits the stages");
   Table& gt = *reinterpret_cast<Table*>(&sm.x[0][0]);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l15 = lane & 15, grp = lane >> 4, wr = wave >> 1, wc = wave & 1;
   const int nb = static_cast<int>((p.N + 127) / 128);
-  int first = 0, last = 0, step = 1, n_rows = 0;
-#pragma clang loop unroll(disable)
-  for (int base = 0;; base += kNarrowDesc) {
-    __syncthreads();
-    for (int g = tid; g < p.El; g += kWideThreads) {
-      int m = p.sizes[p.g0 + g];
-      if (m < 0) {
-        if (blockIdx.x == 0) raise_error(p.err, MOE_DEVERR_GROUP_SIZE);
-        m = 0;
-      }
-      gt.tmp[g] = m;
+  group_table<KIND, kNarrow>(p, gt, tid, kWideThreads, NT);
+  int first, last, step;
+  xcd_share(TG ? p.El * RT * NT : gt.tiles_off[p.El], first, last, step);
+  const int n_rows = gt.rows_off[p.El];
+  const int count = first < last ? (last - first + step - 1) / step : 0;               // this workgroup's tiles
+  if (tid < count) decode_tile<KIND, kNarrow>(p, gt, first + tid * step, RT, NT, sm.desc[tid], sm.more[tid]);
+  __syncthreads();
+  // the loads' place in the stream
+  WideTile lt{};
+  int li = 0, ls = 0, lb = 0, issued = 0;
+  __amdgpu_buffer_rsrc_t xbuf = buffer(p.x, 0), wbuf = xbuf, xsbuf = xbuf, wsbuf = xbuf;
+  const uint8_t *xsrc = nullptr, *wsrc = nullptr;
+  uint32_t odd = 0;
+  auto seek = [&] {
+    ls = 0;
+    for (; li < count; ++li) {
+      lt = narrow_tile(sm, li);
+      if (lt.steps > 0) break;
     }
-    __syncthreads();
-    const bool over = wave0_scan_sat(gt.tmp, gt.rows_off, p.El, p.M);
-    if (over && tid == 0 && blockIdx.x == 0) raise_error(p.err, MOE_DEVERR_ROWS);
-    __syncthreads();
-    for (int g = tid; g < p.El; g += kWideThreads) {
-      const int m = gt.rows_off[g + 1] - gt.rows_off[g];
-      gt.tmp[g] = TG ? (m + 127) / 128 : row_tiles(m, kNarrow) * NT;
+    if (li >= count) return;
+    if constexpr (TG) {
+      xsrc = p.x + 128 * (lt.blk0 * p.K + lt.row0);
+      wsrc = p.w + 128 * (lt.blk0 * p.N + lt.col0);
+    } else {
+      const uint32_t K = static_cast<uint32_t>(p.K), lds = static_cast<uint32_t>(p.lds);
+      const uint32_t cols = static_cast<uint32_t>(min(static_cast<int>(p.N) - lt.col0, kNarrow));
+      xbuf = buffer(p.x + static_cast<int64_t>(lt.row0) * p.ldx, (lt.rows - 1) * static_cast<uint32_t>(p.ldx) + K);
+      wbuf = buffer(p.w + (static_cast<int64_t>(lt.g) * p.N + lt.col0) * p.K, cols * K);
+      xsbuf = buffer(p.xs + lt.row0 * p.lds, lt.rows * lds);
+      const int size = KIND == kGmmF32 ? 4 : 1;
+      const uint8_t* src = static_cast<const uint8_t*>(p.ws) + (static_cast<int64_t>(lt.g) * lt.steps * nb + lt.col0 / 128) * size;
+      odd = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src)) & 3;
+      wsbuf = buffer(src - odd, (static_cast<uint32_t>(lt.steps * nb * size) + odd + 3) & ~3u);
     }
-    __syncthreads();
-    wave0_scan(gt.tmp, TG ? gt.blocks_off : gt.tiles_off, p.El);
-    __syncthreads();
-    xcd_share(TG ? p.El * RT * NT : gt.tiles_off[p.El], first, last, step);
-    n_rows = gt.rows_off[p.El];
-    const int left = first < last ? (last - first + step - 1) / step - base : 0;       // this workgroup's tiles
-    const int count = min(left, kNarrowDesc);
-    if (tid < count) {
-      const int t = first + (base + tid) * step;
-      if (TG) {
-        const int g = t / (RT * NT), l = t - g * RT * NT, rt = l / NT, ct = l - rt * NT;
-        sm.desc[tid] = make_int4(kNarrow * rt, ct, g, min(kNarrow, static_cast<int>(p.K) - kNarrow * rt));
-        sm.more[tid] = make_int2(gt.blocks_off[g + 1] - gt.blocks_off[g], gt.blocks_off[g]);
-      } else {
-        const int g = find_group(gt, p.El, t);
-        const int m = gt.rows_off[g + 1] - gt.rows_off[g], nr = row_tiles(m, kNarrow), fr = tile_frags(m, nr);
-        const int local = t - gt.tiles_off[g], ct = local / nr, rt = local - ct * nr;
-        const int rows = max(min(16 * fr, m - 16 * fr * rt), 0);
-        sm.desc[tid] = make_int4(gt.rows_off[g] + 16 * fr * rt, ct, g, rows);
-        sm.more[tid] = make_int2(rows ? static_cast<int>((p.K + 127) / 128) : 0, 0);
-      }
+  };
+  const int lr = 8 * wave + (lane >> 3);         // the staged row that the lane fills
+  const uint32_t ldx = TG ? 128u : static_cast<uint32_t>(p.ldx), ldw = TG ? 128u : static_cast<uint32_t>(p.K);
+  const uint32_t xc = 16 * ((lane & 7) ^ swz_run(lr)), wch = 16 * ((lane & 7) ^ (OUT_BF16 ? swz_quads(lr) : swz_run(lr)));
+  // one load of each operand a wave; waves 0 and 1 bring the scales as well
+  auto load = [&] {
+    uint32_t xo = lr * ldx + xc, wo = lr * ldw + wch;
+    if (!TG && 128 * ls + 128 > p.K) {
+      const uint32_t end = static_cast<uint32_t>(p.K) - 128u * ls;
+      xo = xc < end ? xo : kNowhere;
+      wo = wch < end ? wo : kNowhere;
     }
-    __syncthreads();
-    // the loads' place in the stream
-    WideTile lt{};
-    int li = 0, ls = 0, lb = 0, issued = 0;
-    __amdgpu_buffer_rsrc_t xbuf = buffer(p.x, 0), wbuf = xbuf, xsbuf = xbuf, wsbuf = xbuf;
-    const uint8_t *xsrc = nullptr, *wsrc = nullptr;
-    uint32_t odd = 0;
-    auto seek = [&] {
-      ls = 0;
-      for (; li < count; ++li) {
-        lt = narrow_tile(sm, li);
-        if (lt.steps > 0) break;
-      }
-      if (li >= count) return;
+    const uint32_t at = TG ? 0u : 128u * ls;
+    if constexpr (TG) {
+      xbuf = buffer(xsrc, 128u * lt.rows);
+      wbuf = buffer(wsrc, 128u * static_cast<uint32_t>(min(static_cast<int>(p.N) - lt.col0, kNarrow)));
+      xsrc += 128 * p.K;
+      wsrc += 128 * p.N;
+    }
+    if (wave == 0) {
       if constexpr (TG) {
-        xsrc = p.x + 128 * (lt.blk0 * p.K + lt.row0);
-        wsrc = p.w + 128 * (lt.blk0 * p.N + lt.col0);
+        const __amdgpu_buffer_rsrc_t b = buffer(p.xs + (static_cast<int64_t>(lt.blk0) + ls) * p.K + lt.row0, static_cast<uint32_t>(lt.rows));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)sm.xs[lb], 4, 4 * lane, 0, 0, 0);
       } else {
-        const uint32_t K = static_cast<uint32_t>(p.K), lds = static_cast<uint32_t>(p.lds);
-        const uint32_t cols = static_cast<uint32_t>(min(static_cast<int>(p.N) - lt.col0, kNarrow));
-        xbuf = buffer(p.x + static_cast<int64_t>(lt.row0) * p.ldx, (lt.rows - 1) * static_cast<uint32_t>(p.ldx) + K);
-        wbuf = buffer(p.w + (static_cast<int64_t>(lt.g) * p.N + lt.col0) * p.K, cols * K);
-        xsbuf = buffer(p.xs + lt.row0 * p.lds, lt.rows * lds);
-        const int size = KIND == kGmmF32 ? 4 : 1;
-        const uint8_t* src = static_cast<const uint8_t*>(p.ws) + (static_cast<int64_t>(lt.g) * lt.steps * nb + lt.col0 / 128) * size;
-        odd = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src)) & 3;
-        wsbuf = buffer(src - odd, (static_cast<uint32_t>(lt.steps * nb * size) + odd + 3) & ~3u);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(xsbuf, (lds_void*)sm.xs[lb], 4, lane * static_cast<uint32_t>(p.lds), ls & ~3, 0, 0);
       }
-    };
-    const int lr = 8 * wave + (lane >> 3);         // the staged row that the lane fills
-    const uint32_t ldx = TG ? 128u : static_cast<uint32_t>(p.ldx), ldw = TG ? 128u : static_cast<uint32_t>(p.K);
-    const uint32_t xc = 16 * ((lane & 7) ^ swz_run(lr)), wch = 16 * ((lane & 7) ^ (OUT_BF16 ? swz_quads(lr) : swz_run(lr)));
-    // one load of each operand a wave; waves 0 and 1 bring the scales as well
-    auto load = [&] {
-      uint32_t xo = lr * ldx + xc, wo = lr * ldw + wch;
-      if (!TG && 128 * ls + 128 > p.K) {
-        const uint32_t end = static_cast<uint32_t>(p.K) - 128u * ls;
-        xo = xc < end ? xo : kNowhere;
-        wo = wch < end ? wo : kNowhere;
-      }
-      const uint32_t at = TG ? 0u : 128u * ls;
+    } else if (wave == 1) {
       if constexpr (TG) {
-        xbuf = buffer(xsrc, 128u * lt.rows);
-        wbuf = buffer(wsrc, 128u * static_cast<uint32_t>(min(static_cast<int>(p.N) - lt.col0, kNarrow)));
-        xsrc += 128 * p.K;
-        wsrc += 128 * p.N;
+        const __amdgpu_buffer_rsrc_t b = buffer(static_cast<const uint8_t*>(p.ws) + (static_cast<int64_t>(lt.blk0) + ls) * p.N + lt.col0,
+                                                static_cast<uint32_t>(min(static_cast<int>(p.N) - lt.col0, kNarrow)));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)sm.ws[lb], 4, 4 * lane, 0, 0, 0);
+      } else {
+        const uint32_t scale_at = KIND == kGmmF32 ? 4u * ls * nb : (odd + ls * nb) & ~3u;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(wsbuf, (lds_void*)sm.ws[lb], 4, scale_at, 0, 0, 0);
       }
-      if (wave == 0) {
-        if constexpr (TG) {
-          const __amdgpu_buffer_rsrc_t b = buffer(p.xs + (static_cast<int64_t>(lt.blk0) + ls) * p.K + lt.row0, static_cast<uint32_t>(lt.rows));
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)sm.xs[lb], 4, 4 * lane, 0, 0, 0);
-        } else {
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(xsbuf, (lds_void*)sm.xs[lb], 4, lane * static_cast<uint32_t>(p.lds), ls & ~3, 0, 0);
-        }
-      } else if (wave == 1) {
-        if constexpr (TG) {
-          const __amdgpu_buffer_rsrc_t b = buffer(static_cast<const uint8_t*>(p.ws) + (static_cast<int64_t>(lt.blk0) + ls) * p.N + lt.col0,
-                                                  static_cast<uint32_t>(min(static_cast<int>(p.N) - lt.col0, kNarrow)));
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)sm.ws[lb], 4, 4 * lane, 0, 0, 0);
-        } else {
-          const uint32_t scale_at = KIND == kGmmF32 ? 4u * ls * nb : (odd + ls * nb) & ~3u;
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(wsbuf, (lds_void*)sm.ws[lb], 4, scale_at, 0, 0, 0);
-        }
-      }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wbuf, (lds_void*)(sm.w[lb] + 1024 * wave), 16, wo, at, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xbuf, (lds_void*)(sm.x[lb] + 1024 * wave), 16, xo, at, 0, 0);
-      order();
-      lb = lb + 1 == NST ? 0 : lb + 1;
-      ++issued;
-      if (++ls == lt.steps) {
-        ++li;
-        seek();
-      }
-    };
-    seek();
+    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(wbuf, (lds_void*)(sm.w[lb] + 1024 * wave), 16, wo, at, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(xbuf, (lds_void*)(sm.x[lb] + 1024 * wave), 16, xo, at, 0, 0);
+    order();
+    lb = lb + 1 == NST ? 0 : lb + 1;
+    ++issued;
+    if (++ls == lt.steps) {
+      ++li;
+      seek();
+    }
+  };
+  seek();
 #pragma unroll
-    for (int j = 0; j < NST - 1; ++j)
+  for (int j = 0; j < NST - 1; ++j)
+    if (li < count) load();
+  const int wrow = 32 * wc + frag_col<OUT_BF16>(0, l15);
+  const uint32_t xa0 = lds_addr(sm.x[0]) + (16 * wr + l15) * 128 + 16 * (grp ^ swz_run(l15));
+  const uint32_t wa0 = lds_addr(sm.w[0]) + wrow * 128 + 16 * (grp ^ (OUT_BF16 ? swz_quads(wrow) : swz_run(wrow)));
+  int done = 0, b = 0;
+#pragma clang loop unroll(disable)
+  for (int i = 0; i < count; ++i) {
+    const WideTile t = narrow_tile(sm, i);
+    v4f acc[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
+#pragma clang loop unroll(disable)
+    for (int s = 0; s < t.steps; ++s) {
+      // the stage is there when at most the six behind it are outstanding (and what was stored before them)
+      if (issued - done < NST - 1)
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+      else if (wave < 2)
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(3 * (NST - 2)));
+      else
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * (NST - 2)));
+      step_barrier();                            // every wave's loads are; the stage before is read
       if (li < count) load();
-    const int wrow = 32 * wc + frag_col<OUT_BF16>(0, l15);
-    const uint32_t xa0 = lds_addr(sm.x[0]) + (16 * wr + l15) * 128 + 16 * (grp ^ swz_run(l15));
-    const uint32_t wa0 = lds_addr(sm.w[0]) + wrow * 128 + 16 * (grp ^ (OUT_BF16 ? swz_quads(wrow) : swz_run(wrow)));
-    int done = 0, b = 0;
-#pragma clang loop unroll(disable)
-    for (int i = 0; i < count; ++i) {
-      const WideTile t = narrow_tile(sm, i);
-      v4f acc[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
-#pragma clang loop unroll(disable)
-      for (int s = 0; s < t.steps; ++s) {
-        // the stage is there when at most the six behind it are outstanding (and what was stored before them)
-        if (issued - done < NST - 1)
-          __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-        else if (wave < 2)
-          __builtin_amdgcn_s_waitcnt(waitcnt_vm(3 * (NST - 2)));
-        else
-          __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * (NST - 2)));
-        step_barrier();                            // every wave's loads are; the stage before is read
-        if (li < count) load();
-        ++done;
-        if (16 * wr < t.rows) {
-          const uint32_t xa = xa0 + b * static_cast<uint32_t>(sizeof(sm.x[0])), wa = wa0 + b * static_cast<uint32_t>(sizeof(sm.w[0]));
-          const v8i x = frag(__builtin_bit_cast(uint4, lds_read<v4i>(xa)), __builtin_bit_cast(uint4, lds_read<v4i>(xa ^ 64u)));
-          const uint32_t xsa = lds_addr(sm.xs[0]) + b * static_cast<uint32_t>(sizeof(sm.xs[0])), wsa = lds_addr(sm.ws[0]) + b * static_cast<uint32_t>(sizeof(sm.ws[0]));
-          uint32_t xs, ws[2];
-          float factor = 1.0f;
-          if constexpr (TG) {
-            xs = lds_read<uint8_t>(xsa + 16 * wr + l15);
+      ++done;
+      if (16 * wr < t.rows) {
+        const uint32_t xa = xa0 + b * static_cast<uint32_t>(sizeof(sm.x[0])), wa = wa0 + b * static_cast<uint32_t>(sizeof(sm.w[0]));
+        const v8i x = frag(__builtin_bit_cast(uint4, lds_read<v4i>(xa)), __builtin_bit_cast(uint4, lds_read<v4i>(xa ^ 64u)));
+        const uint32_t xsa = lds_addr(sm.xs[0]) + b * static_cast<uint32_t>(sizeof(sm.xs[0])), wsa = lds_addr(sm.ws[0]) + b * static_cast<uint32_t>(sizeof(sm.ws[0]));
+        uint32_t xs, ws[2];
+        float factor = 1.0f;
+        if constexpr (TG) {
+          xs = lds_read<uint8_t>(xsa + 16 * wr + l15);
 #pragma unroll
-            for (int f = 0; f < 2; ++f) ws[f] = lds_read<uint8_t>(wsa + wrow + frag_col<OUT_BF16>(f, 0));
+          for (int f = 0; f < 2; ++f) ws[f] = lds_read<uint8_t>(wsa + wrow + frag_col<OUT_BF16>(f, 0));
+        } else {
+          xs = lds_read<uint32_t>(xsa + 4 * (16 * wr + l15)) >> (8 * (s & 3));
+          if constexpr (KIND == kGmmF32) {
+            const F32Scale sc = split_scale(lds_read<uint32_t>(wsa));
+            factor = sc.factor;
+            xs = lowered(xs & 255u, sc.down);
+            ws[0] = ws[1] = sc.code;
           } else {
-            xs = lds_read<uint32_t>(xsa + 4 * (16 * wr + l15)) >> (8 * (s & 3));
-            if constexpr (KIND == kGmmF32) {
-              const F32Scale sc = split_scale(lds_read<uint32_t>(wsa));
-              factor = sc.factor;
-              xs = lowered(xs & 255u, sc.down);
-              ws[0] = ws[1] = sc.code;
-            } else {
-              const uint32_t byte = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.ws)) + (static_cast<uint32_t>(t.g) * t.steps + s) * nb + t.col0 / 128) & 3;
-              ws[0] = ws[1] = lds_read<uint8_t>(wsa + byte);
-            }
-          }
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const uint32_t at = frag_col<OUT_BF16>(f, 0) * 128;
-            const v8i w = frag(__builtin_bit_cast(uint4, lds_read<v4i>(wa + at)), __builtin_bit_cast(uint4, lds_read<v4i>((wa ^ 64u) + at)));
-            if constexpr (KIND == kGmmF32)
-              acc[f] += factor * mfma_scaled(w, ws[f], x, xs, v4f{0.f, 0.f, 0.f, 0.f});
-            else
-              acc[f] = mfma_scaled(w, ws[f], x, xs, acc[f]);
+            const uint32_t byte = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.ws)) + (static_cast<uint32_t>(t.g) * t.steps + s) * nb + t.col0 / 128) & 3;
+            ws[0] = ws[1] = lds_read<uint8_t>(wsa + byte);
           }
         }
-        b = b + 1 == NST ? 0 : b + 1;
-      }
-      if (16 * wr + l15 < t.rows) {
-        const int64_t row = (TG ? t.g * p.K + t.row0 : t.row0) + 16 * wr + l15;
-        if (OUT_BF16) {
-          const int64_t c = t.col0 + 32 * wc + 8 * grp;
-          if (c < p.N)
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.N + c) =
-                make_uint4(pack_bf16(acc[0][0], acc[0][1]), pack_bf16(acc[0][2], acc[0][3]), pack_bf16(acc[1][0], acc[1][1]), pack_bf16(acc[1][2], acc[1][3]));
-        } else {
 #pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const int64_t c = t.col0 + 32 * wc + 16 * f + 4 * grp;
-            if (c < p.N) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.N + c) = make_float4(acc[f][0], acc[f][1], acc[f][2], acc[f][3]);
-          }
+        for (int f = 0; f < 2; ++f) {
+          const uint32_t at = frag_col<OUT_BF16>(f, 0) * 128;
+          const v8i w = frag(__builtin_bit_cast(uint4, lds_read<v4i>(wa + at)), __builtin_bit_cast(uint4, lds_read<v4i>((wa ^ 64u) + at)));
+          if constexpr (KIND == kGmmF32)
+            acc[f] += factor * mfma_scaled(w, ws[f], x, xs, v4f{0.f, 0.f, 0.f, 0.f});
+          else
+            acc[f] = mfma_scaled(w, ws[f], x, xs, acc[f]);
+        }
+      }
+      b = b + 1 == NST ? 0 : b + 1;
+    }
+    if (16 * wr + l15 < t.rows) {
+      const int64_t row = (TG ? t.g * p.K + t.row0 : t.row0) + 16 * wr + l15;
+      if (OUT_BF16) {
+        const int64_t c = t.col0 + 32 * wc + 8 * grp;
+        if (c < p.N)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.N + c) =
+              make_uint4(pack_bf16(acc[0][0], acc[0][1]), pack_bf16(acc[0][2], acc[0][3]), pack_bf16(acc[1][0], acc[1][1]), pack_bf16(acc[1][2], acc[1][3]));
+      } else {
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int64_t c = t.col0 + 32 * wc + 16 * f + 4 * grp;
+          if (c < p.N) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.N + c) = make_float4(acc[f][0], acc[f][1], acc[f][2], acc[f][3]);
         }
       }
     }
-    if (left <= kNarrowDesc) break;
   }
   if constexpr (!TG) zero_rows<OUT_BF16, kWideThreads>(p, n_rows);
 }

@@ -41,3 +41,19 @@ def test_the_rule_at_its_borders():
     assert rule.gradient_kernel(255, 256, 256) == "narrow" and rule.gradient_kernel(256, 16, 16) == "wide"
     # no local expert, and more experts than rows
     assert rule.product_kernel(0, 5, 32) == "few16" and rule.product_kernel(1000, 3, 1024) == "few16"
+
+
+@pytest.mark.parametrize("cus", [8, 15, 32, 80, 228, 256, 304])
+def test_narrow_tiles_are_decoded_at_once(cus):
+    """However the rows fall, a workgroup of the narrow kernel has at most the 64 tiles that its table holds: the worst split of M
+    rows into El groups makes M / 64 + groups row tiles, and an XCD's share of all tiles goes to cus / 8 workgroups at least."""
+    import random
+    rng, worst = random.Random(cus), 0
+    for _ in range(20000):
+        El, M, N = rng.choice((1, 2, 3, 8, 32, 64, 256, 1000)), int(2 ** rng.uniform(0, 17)), 16 * int(2 ** rng.uniform(0, 10))
+        if rule.product_kernel(El, M, N, cus) == "narrow":
+            worst = max(worst, -(-((M // 64 + min(El, M)) * -(-N // 64)) // 8) / (cus // 8))
+        Kdim = 16 * int(2 ** rng.uniform(0, 10))
+        if rule.gradient_kernel(El, Kdim, N, cus) == "narrow":
+            worst = max(worst, -(-(El * -(-Kdim // 64) * -(-N // 64)) // 8) / (cus // 8))
+    assert 2 < worst and -(-worst // 1) <= 64
