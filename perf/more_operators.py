@@ -228,6 +228,8 @@ def prepare(case, seed):
             st["dloss"] = torch.rand(S, generator=gen, device=DEV) + 0.5
             st["counts"], st["tokens"] = _counts(st)
             st["dlogits"] = torch.zeros_like(z)
+    if own:
+        st["workspace"] = _workspace(case)
     return st
 
 
@@ -340,20 +342,20 @@ def _balance_bwd(st):
 
 
 # ----------------------------------------------------------------- one pass
-_kept = {}
-
-
-def _workspace(m, op, d0, d1, d2, E):
-    """The workspace that a program keeps from call to call."""
-    key = (op, d0, d1, d2, E)
-    if key not in _kept:
-        _kept[key] = m.workspace(op, d0, d1, d2, E)
-    return _kept[key]
+def _workspace(case):
+    """The workspace that a program keeps beside its buffers (and a pass on another stream has one of its own)."""
+    import moe_fp8_grouped_amd as m
+    if case["op"] in ("product", "wgrad"):
+        op = m.MOE_OP_GMM_B128 if case["op"] == "product" else m.MOE_OP_TGMM_B128
+        return m.workspace(op, case["T"] * case["k"], case["K"], case["N"], case["E"])
+    return m.workspace(m.MOE_OP_BALANCE, case["T"], case["S"], 0, case["E"]) if case["op"] == "balance" else None
 
 
 def _own(st):
     import moe_fp8_grouped_amd as m
     c, op = st["case"], st["case"]["op"]
+    if "workspace" not in st:
+        st["workspace"] = _workspace(c)
     if op == "rows":
         R, C, rows, up = c["R"], c["C"], st["rows"], st["up"]
         ld, kb = rows.shape[1], -(-C // B)
@@ -368,12 +370,12 @@ def _own(st):
         ld, kb = rows.shape[1], -(-K // B)
         m.moe_gmm_b128(rows[:, :K], ld, rows[:, K:K + kb], ld, st["w"], st["ws"],
                        m.MOE_E8M0 if c["scales"] == "e8m0" else m.MOE_F32, st["sizes"], E, 0, E, M, K, N, m.MOE_BF16,
-                       st["out"], _workspace(m, m.MOE_OP_GMM_B128, M, K, N, E))
+                       st["out"], st["workspace"])
         return st["out"]
     if op == "wgrad":
         T, k, E, K, N = (c[n] for n in ("T", "k", "E", "K", "N"))
         M, x, sizes = T * k, st["x"], st["sizes"]
-        ws = _workspace(m, m.MOE_OP_TGMM_B128, M, K, N, E)
+        ws = st["workspace"]
         if c["gated"]:
             m.moe_quantize_cols_b128(x[:, :K], x[:, K:], 2 * K, m.MOE_ACT_SILU_MUL, M, 1, None, sizes, E, 0, E, M, K,
                                      st["xt"], st["xt_s"], ws)
@@ -389,7 +391,7 @@ def _own(st):
     score = m.MOE_SCORE_SIGMOID if c["score"] == "sigmoid" else m.MOE_SCORE_SOFTMAX
     if op == "balance":
         m.moe_balance_loss(z, dt, E, st["ids"], T, E, k, score, st["offsets"], S, st["loss"], st["counts"], st["tokens"],
-                           _workspace(m, m.MOE_OP_BALANCE, T, S, 0, E))
+                           st["workspace"])
         return st["loss"], st["counts"], st["tokens"]
     m.moe_balance_loss_backward(z, dt, E, st["counts"], st["tokens"], st["dloss"], T, E, k, score, st["offsets"], S, 0,
                                 st["dlogits"], E)
