@@ -837,7 +837,7 @@ int moe_tgmm_b128(const uint8_t* lhs_t, const uint8_t* lhs_scale, const uint8_t*
  * expert, c[e] choices of expert e:
  *   loss[s] = E / (k n^2) * sum_e c[e] * sum_t p[t, e]         (0 where n = 0)
  * which is 1 where either is even over the experts.  A share is held in float32,
- * off by a few units in its last place (exponentials and quotients as the router's).
+ * off by a few units in its last place (0 below 2^-126 of the row's largest).
  *   logits, logits_dtype, ldl  [T, E] as in moe_router_topk.  A logit of -inf or
  *            NaN, or at or below -1e30 (a mask of the type's lowest value), takes
  *            its expert out for that token: no share, and no choice of it counts.

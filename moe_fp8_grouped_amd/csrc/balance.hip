@@ -69,21 +69,37 @@ __device__ __forceinline__ float over_row(float v) {
   return G == 16 ? row_sum(v) : sum_of(v);
 }
 
+// exp(x), x <= 0, within 1.5 units in the last place (0 below 2^-126): x log2 e as a sum of two floats, the power of two of the
+// larger by the hardware, corrected by 1 + ln 2 times the smaller.  (The power of the rounded product alone is off by up
+// to 58 units of 2^-24 at x = -84.  With expf and IEEE quotients the loss of 8192 tokens of 256 experts takes 17.5 us where this takes
+// 16.8, the gradient of 32768 sigmoid rows of 64 experts 9.2 where this takes 7.5; with the rounded product 16.0 and 7.3.)
+__device__ __forceinline__ float exp_of(float x) {
+  x = fmaxf(x, -150.0f);
+  const float h = x * 0x1.715476p+0f;
+  const float l = fmaf(x, 0x1.4ae0cp-26f, fmaf(x, 0x1.715476p+0f, -h));
+  const float e = __builtin_amdgcn_exp2f(h);
+  return fmaf(e, l * 0x1.62e43p-1f, e);
+}
+// 1 / x for x from 1/2 to 2^11, within half a unit (and 2^-22 of one): the hardware's estimate and one step of Newton's.
+__device__ __forceinline__ float inverse_of(float x) {
+  const float y = __builtin_amdgcn_rcpf(x);
+  return fmaf(fmaf(-x, y, 1.0f), y, y);
+}
+
 // A score up to a factor common to the row, with m its largest logit: exp(z - m), or
 // sigmoid(z) / exp(min(m, 0)) = exp(min(z, 0) - min(m, 0)) / (1 + exp(-|z|)),
 // which stays in range where every sigmoid of the row is below it.  0 for an
-// expert taken out.  (expf and quotients as in the router: the hardware's power of
-// two would take |z - m| log2 e rounded, up to 57 units of 2^-24 of a share at z - m = -80; it saved 1.2 us.)
+// expert taken out.
 template <bool SIGMOID>
 __device__ __forceinline__ float score(float z, float m, float& rest) {
   if (z == -INFINITY) return 0.0f;
   if constexpr (SIGMOID) {
-    const float e = expf(-fabsf(z)), d = 1.0f / (1.0f + e);
+    const float e = exp_of(-fabsf(z)), d = inverse_of(1.0f + e);
     rest = z < 0.0f ? d : e * d;
-    return (z < 0.0f ? expf(z - fminf(m, 0.0f)) : 1.0f) * d;
+    return (z < 0.0f ? exp_of(z - fminf(m, 0.0f)) : 1.0f) * d;
   } else {
     rest = 1.0f;
-    return expf(z - m);
+    return exp_of(z - m);
   }
 }
 
@@ -186,7 +202,7 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const BalanceArgs p, 
             q[i][c] = score<SIGMOID>(row[u].z[i][c], m, rest);
             sum += q[i][c];
           }
-        const float inv = 1.0f / over_row<G>(sum);
+        const float inv = inverse_of(over_row<G>(sum));
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -341,7 +357,7 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(const BalanceArgs p, c
       }
     sum = over_row<G>(sum);
     dot = over_row<G>(dot);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum > 0.0f ? inverse_of(sum) : 0.0f;
     if (!in) continue;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -400,9 +416,9 @@ size_t balance_ws_bytes(int64_t T, int64_t S, int E) {
 
 }  // namespace moe
 
-// Sixteen lanes a row up to 128 experts, the whole wave above.  Loss and gradient of 8192 tokens as graphs, us: 64 experts
-// 11.9 and 4.5 (a wave a row 14.2 and 5.7), 128 experts 13.1 and 5.3 (14.6 and 6.0), 256 experts 14.4 and 6.5 (sixteen lanes
-// 14.9 and 7.4); of 32768 tokens, 64 experts, 13.2 and 7.2 (16.1 and 14.1).
+// Sixteen lanes a row up to 128 experts, the whole wave above.  Loss and gradient of 8192 tokens in 5 sequences as graphs, us: 64 experts
+// 12.1 and 4.4 (a wave a row 15.2 and 5.4), 128 experts 14.1 and 5.2 (16.1 and 5.7), 256 experts 16.8 and 6.1 (sixteen lanes
+// 17.0 and 7.1); of 32768 tokens, 64 experts, 14.7 and 7.1 (18.8 and 13.7).
 #define MOE_BY_V(CALL, B, S)                                      \
   do {                                                            \
     if (E <= 64) CALL(B, S, 16, 1);                               \

@@ -2,10 +2,10 @@
 each a sequence of its own, the rarer one chosen, so that the loss is twice
 that expert's share and no sum hides an error.
 
-Tolerances (u = 2^-24), for logits whose differences are exact.  expf is within
-2 ulp, 4 u.  Softmax: 4 u, the sum, its inverse, the product and the loss u each:
-8 u.  Sigmoid scores exp(z) / (1 + exp(z)) for z < 0: exp(z) 4 u, the denominator
-2 u (half of an exponential's 4 u at most) + u, its inverse u and a product u, 9 u;
+Tolerances (u = 2^-24), for logits whose differences are exact.  An exponential
+is within 2 ulp, 4 u, an inverse within u.  Softmax: 4 u, the sum, its inverse, the product
+and the loss u each: 8 u.  Sigmoid scores exp(z) / (1 + exp(z)) for z < 0: exp(z) 4 u, the
+denominator 2 u (half of an exponential's 4 u at most) + u, its inverse u and a product u, 9 u;
 the other score 4 u, then 4 u as above: 17 u.  The gradient is twice p (1 - p)
 (times 1 - sigmoid): p as above less the loss's u; the difference of
 the counts from their mean weighted by the shares: at most 8 u of magnitudes
