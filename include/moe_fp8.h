@@ -849,7 +849,8 @@ int moe_tgmm_b128(const uint8_t* lhs_t, const uint8_t* lhs_scale, const uint8_t*
  *            seq_offsets[s] .. seq_offsets[s+1] - 1 (it may be empty); rows
  *            outside all sequences take no part.  NULL with S = 1: all T rows.
  *            Offsets that decrease or leave [0, T] set MOE_DEVERR_SEQUENCE and
- *            are clamped.
+ *            are clamped; where they decrease, what the call writes for the
+ *            sequences is unspecified.
  *   loss     [S] f32 out; counts [S, E] int32 out; tokens [S] int32 out: n.
  *   ws       workspace of moe_workspace_bytes(MOE_OP_BALANCE, T, S, 0, E).
  * The result's bits do not depend on the order in which the device runs.

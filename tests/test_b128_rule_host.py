@@ -57,3 +57,11 @@ def test_narrow_tiles_are_decoded_at_once(cus):
         if rule.gradient_kernel(El, Kdim, N, cus) == "narrow":
             worst = max(worst, -(-(El * -(-Kdim // 64) * -(-N // 64)) // 8) / (cus // 8))
     assert 2 < worst and -(-worst // 1) <= 64
+
+
+def test_the_large_layer_runs_the_wide_kernels():
+    from tests.test_gpu_block_scaled_ffn_wide import CASE
+    M, El, H, I = CASE["T"] * CASE["k"], CASE["El"], CASE["H"], CASE["I"]
+    products = [2 * I, H, I, H]                             # forward up and down, then to h and to x
+    kernels = [rule.product_kernel(El, M, N) for N in products] + [rule.gradient_kernel(El, I, H), rule.gradient_kernel(El, H, 2 * I)]
+    assert kernels == ["wide", "wide", "narrow", "wide", "wide", "wide"], kernels
