@@ -3,9 +3,10 @@
 // by 128, and of 128 along a group's rows (b128_common.hpp).  v / scale is exact,
 // the scale a power of two, so a code is v's nearest with one rounding.  Memory
 // bounds all three: 2 bytes in, 1 out (2 for weights in both orientations).
-// Measured: rows of 8192 x 7168 31 us (5.7 TB/s); weights of 8 x 7168 x 2048 96 us
-// (4.9 TB/s); columns of 32768 x 1536 46 us (3.3 TB/s), of 32768 x 4096 gathered from
-// 8192 tokens 78 us (2.6 TB/s of the bytes that leave the caches).
+// Measured: rows of 8192 x 7168 31 us (5.7 TB/s), gated 62 to 74 (4.0 to 4.7); weights of
+// 8 x 7168 x 2048 96 us (4.9 TB/s); columns of 32768 x 1536 51 us (3.0 TB/s; 30 where the
+// rows lie in the caches), gated 73 (3.4), of 32768 x 4096 gathered from 8192 tokens 80 us
+// (2.5 TB/s of the bytes that leave the caches).
 #include "b128_common.hpp"
 #include "quant_common.hpp"
 

@@ -24,8 +24,11 @@ inline int64_t few_tiles(int64_t El, int64_t M, int rows) {
 // tiles 27), 64 rows 23 (33), 128 rows 42 (33); 64 groups of 2048 by 1536: 8 rows 11 (12), 16 rows 19 (19), 32 rows 31 (26).
 //
 // Wide tiles where every workgroup has one: 128 rows in 64 groups of 2048 x 1536 take 41 us (narrow ones 44 to 47), the weight
-// gradient of 512 rows in 8 groups, 2080 x 1040, 19 us (narrow ones 29); 512 rows in 8 groups of 2080 x 1040, 20 tiles, take 13 us
-// with narrow ones (19).
+// gradient of 512 rows in 8 groups, 2080 x 1040, 19 us (narrow ones 29); 512 rows in 8 groups of 2080 x 1040, 20 tiles, take 12.4 us
+// with narrow ones (wide ones 22), 2048 rows in 8 groups of 2048 x 1536, 84 tiles, 30 (35).  The rule errs where tiles are full and
+// somewhat fewer than CUs (one group of 4096 rows, 8192 x 4096, 208 tiles: 493 us, wide ones 136; of 2048 rows, 4096 x 4096, 112
+// tiles: 131, wide ones 71; of 1024, 64 tiles: 67 and 61), and where rows, which it cannot see, are in few of the groups that it
+// counts (128 rows in one of 64 groups of 2048 x 1536: 25 us, narrow ones 12; 2048 in one: 39 and 29; evenly: 38 and 43).
 inline Choice product_kernel(int64_t El, int64_t M, int64_t N, int cus) {
   const int rows = El == 1 && M > 32 ? 64 : El == 1 && M > 16 ? 32 : 16;
   if (few_tiles(El, M, rows) * (N / 16) * (rows / 16) <= 6 * static_cast<int64_t>(cus)) return rows == 64 ? kFew64 : rows == 32 ? kFew32 : kFew16;

@@ -6,8 +6,8 @@
 //   dz[t, e] = dloss E / (k n^2) p_e (c[e] - sum_f c[f] p_f) r_e
 // r = 1 for softmax shares, 1 - sigmoid(z) for normalised sigmoids.
 // Launches and a chunk's chain of loads and sums bound the loss, not its bytes: 8192
-// tokens of 256 experts in bf16 take 15 us, 9 for the chunks (0.5 TB/s) and 6 to join
-// them; the gradient of 32768 tokens of 64 experts 7.3 us (2.3 TB/s).
+// tokens of 256 experts in bf16 take 17 us, 9.4 for the chunks (0.5 TB/s) and 6.8 to
+// join them; the gradient of 32768 tokens of 64 experts 7.5 us (2.2 TB/s).
 #include "wave_common.hpp"
 
 namespace moe {

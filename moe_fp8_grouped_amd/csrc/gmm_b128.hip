@@ -14,13 +14,15 @@
 //
 // Three kernels, by a rule on sizes alone (b128_rule.hpp):
 //   few      few pieces of 16 rows (or up to 64) by 16 columns: every weight is met by a row or a few; latency and the
-//            weights' bytes decide.  One row of 7168 x 4096: 8.2 us (29 MB, 3.6 TB/s).
-//   wide     at least a tile for every workgroup: LDS reads (1536 clocks a 256 x 256 x 128 step), its fill (512) and the
-//            matrix instructions (2048) share the time, and few rows leave the weights' bytes.  32768 rows in 64 groups of
-//            2048 x 1536: 140 us (1.5 PFLOP/s); 8192 rows in 32 of 7168 x 4096: 271 us (1.8 PFLOP/s); 128 rows in 64 of
-//            2048 x 1536: 41 us (4.9 TB/s of weights; narrow tiles 44).  tgmm, 32768 rows in 64 groups, 4096 x 1536 bf16
-//            results: 310 us, of which 190 are left without the stores (0.8 GB, 118 us to a plain fill): they do not overlap.
-//   narrow   fewer tiles than that: the latency of a tile's stages.  512 ragged rows in 8 groups of 2080 x 1040: 13 us (wide
+//            weights' bytes decide.  One row of 7168 x 4096: 8.6 us (29 MB, 3.4 TB/s).
+//   wide     at least a tile for every workgroup: a 256 x 256 x 128 step takes 4050 clocks where its LDS reads take 1630, its
+//            fill 512 and the matrix instructions 2048 (counters): they go in turn.  With operands in L2 3100 to 3450; with
+//            float32 scales, 16 products of a sum with the change of units for every four matrix instructions, 5000.
+//            32768 rows in 64 groups of 2048 x 1536, three tiles of 16 steps a workgroup: e8m0 134 us (1.5 PFLOP/s; 94 in steps,
+//            25 in stores), float32 143; 8192 rows in 32 of 7168 x 4096: 271 us (1.8 PFLOP/s); 128 rows in 64 of
+//            2048 x 1536: 43 us (4.2 TB/s of weights).  tgmm, 32768 rows in 64 groups, 4096 x 1536: bf16 results 290 to
+//            300 us, of which 190 are left without the stores (0.8 GB, 118 us to a plain fill): they do not overlap; float32 400.
+//   narrow   fewer tiles than that: the latency of a tile's stages.  512 ragged rows in 8 groups of 2080 x 1040: 12.5 us (wide
 //            tiles 22); 256 rows in 32 groups of 4096 x 1536: 46 us (4.4 TB/s).
 #include <type_traits>
 
