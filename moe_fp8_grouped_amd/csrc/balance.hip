@@ -6,7 +6,7 @@
 //   dz[t, e] = dloss E / (k n^2) p_e (c[e] - sum_f c[f] p_f) r_e
 // r = 1 for softmax shares, 1 - sigmoid(z) for normalised sigmoids.
 // Launches and a chunk's chain of loads and sums bound the loss, not its bytes: 8192
-// tokens of 256 experts in bf16 take 17 us, 9.4 for the chunks (0.5 TB/s) and 6.8 to
+// tokens of 256 experts in bf16 take 16 us, 9.4 for the chunks (0.5 TB/s) and 6.8 to
 // join them; the gradient of 32768 tokens of 64 experts 7.5 us (2.2 TB/s).
 #include "wave_common.hpp"
 

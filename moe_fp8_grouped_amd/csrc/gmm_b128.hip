@@ -19,7 +19,7 @@
 //            fill 512 and the matrix instructions 2048 (counters): they go in turn.  With operands in L2 3100 to 3450; with
 //            float32 scales, 16 products of a sum with the change of units for every four matrix instructions, 5000.
 //            32768 rows in 64 groups of 2048 x 1536, three tiles of 16 steps a workgroup: e8m0 134 us (1.5 PFLOP/s; 94 in steps,
-//            25 in stores), float32 143; 8192 rows in 32 of 7168 x 4096: 271 us (1.8 PFLOP/s); 128 rows in 64 of
+//            25 in stores), float32 142; 8192 rows in 32 of 7168 x 4096: 271 us (1.8 PFLOP/s); 128 rows in 64 of
 //            2048 x 1536: 43 us (4.2 TB/s of weights).  tgmm, 32768 rows in 64 groups, 4096 x 1536: bf16 results 290 to
 //            300 us, of which 190 are left without the stores (0.8 GB, 118 us to a plain fill): they do not overlap; float32 400.
 //   narrow   fewer tiles than that: the latency of a tile's stages.  512 ragged rows in 8 groups of 2080 x 1040: 12.5 us (wide
